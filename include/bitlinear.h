@@ -263,6 +263,142 @@ bl_status bitlinear_backward_input(const void *grad_y, int gy_dtype, const uint8
 bl_status bitlinear_backward_weight(const void *grad_y, const void *x, int dtype, int64_t M,
                                     int64_t N, int64_t K, float *grad_w, void *stream);
 
+/* ---- Products with bias, activation and residual in the epilogue ----------
+ *
+ *   z[m,n] = gamma * scale[m] / 127 * acc[m,n] + bias[n]
+ *   y[m,n] = act(z[m,n]) + res_scale * residual[m,n]
+ *
+ * acc is the exact INT32 sum of bitlinear_forward; everything after it is fp32,
+ * rounded once to y's type. Activations: BL_ACT_NONE z; BL_ACT_RELU max(z, 0);
+ * BL_ACT_RELU2 max(z, 0)^2; BL_ACT_SILU z / (1 + e^-z); BL_ACT_GELU
+ * z (1 + erf(z / sqrt 2)) / 2; BL_ACT_GELU_TANH z (1 + tanh(sqrt(2 / pi) (z +
+ * 0.044715 z^3))) / 2. (The pages keep the block's nonlinear parts in high
+ * precision, [b158] §3.3.) */
+typedef enum {
+    BL_ACT_NONE = 0,
+    BL_ACT_RELU = 1,
+    BL_ACT_RELU2 = 2,
+    BL_ACT_SILU = 3,
+    BL_ACT_GELU = 4,
+    BL_ACT_GELU_TANH = 5
+} bl_act;
+
+/* bitlinear_forward_epilogue: the product of bitlinear_forward_segmented (one
+ * segment for a plain matrix) with that epilogue.
+ *   bias      [N] bias_dtype, or NULL.
+ *   residual  [M, N] of y's type, or NULL; y itself may be passed, to add in
+ *             place. res_scale (finite) is ignored without it.
+ *   z         optional out: [M, N] of y's type, the pre-activation (what
+ *             bitlinear_epilogue_backward reads), or NULL.
+ * Other arguments, limits, dispatch and errors as for
+ * bitlinear_forward_segmented. Apart from residual and y, no output may
+ * overlap another argument. */
+bl_status bitlinear_forward_epilogue(const int8_t *xq, const float *scale, const uint8_t *packed,
+                                     int layout, const float *gammas, const int64_t *seg_rows,
+                                     int nseg, int64_t M, int64_t K, const void *bias,
+                                     int bias_dtype, int act, const void *residual,
+                                     float res_scale, void *z, void *y, int y_dtype,
+                                     void *stream);
+
+/* bitlinear_linear_epilogue: the same from unquantised x, fused into one
+ * launch as bitlinear_linear (1 <= M <= 4, else BL_ERR_UNSUPPORTED). */
+bl_status bitlinear_linear_epilogue(const void *x, int x_dtype, const uint8_t *packed, int layout,
+                                    const float *gammas, const int64_t *seg_rows, int nseg,
+                                    int64_t M, int64_t K, const void *bias, int bias_dtype,
+                                    int act, const void *residual, float res_scale, void *z,
+                                    void *y, int y_dtype, void *stream);
+
+/* Device workspace (bytes) of bitlinear_epilogue_backward; 0 for an empty or
+ * refused shape. */
+size_t bitlinear_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+
+/* Backward of the epilogue:
+ *   grad_z = grad_y * act'(z);  grad_bias[n] = sum_m grad_z[m,n];
+ *   grad_residual = res_scale * grad_y.
+ * grad_z is what bitlinear_backward_input and _weight take as their grad_y.
+ *   grad_y   [M, N] gy_dtype.   z: [M, N] z_dtype; may be NULL for BL_ACT_NONE.
+ *   grad_z   out [M, N] gz_dtype, or NULL.
+ *   grad_bias out [N] fp32, or NULL: fp32 sums of the unrounded grad_z over at
+ *            most 512 tokens at a time, added in fp64 in a fixed order. Needs the workspace.
+ *   grad_residual out [M, N] gy_dtype, or NULL.
+ * relu's slope at 0 is 0. At least one output is required; outputs may not
+ * overlap inputs. M, N at most 2^24. M = 0 writes zeros to grad_bias. */
+bl_status bitlinear_epilogue_backward(const void *grad_y, int gy_dtype, const void *z, int z_dtype,
+                                      int act, float res_scale, int64_t M, int64_t N, void *grad_z,
+                                      int gz_dtype, float *grad_bias, void *grad_residual,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Norms before and after a block ----------------------------------------
+ *
+ * What stands between two blocks of a transformer layer, in one pass over the
+ * residual stream h [M, K] and the block's output [M, K]:
+ *   p  = norm_post(block)
+ *   h' = res_scale * h + gate * p
+ *   n  = norm_pre(h')
+ * norm(x) = (x - mu) * weight / sqrt(var + eps) + bias over each row, with
+ * mu = mean(x), var = mean((x - mu)^2) for BL_NORM_LAYER and mu = 0, var =
+ * mean(x^2) for BL_NORM_RMS; BL_NORM_NONE leaves x as it is (no weight, no
+ * bias). n is the input of the next BitLinear layer ([QAT-en] "The BitLinear
+ * Recipe": activations are normalised, then quantised); it can leave as
+ * values, as the INT8 codes and scale of bitlinear_quant_acts, or both. */
+typedef enum { BL_NORM_NONE = 0, BL_NORM_RMS = 1, BL_NORM_LAYER = 2 } bl_norm;
+/* BL_GATE_CHANNEL: [K] of p_dtype, shared by the tokens. BL_GATE_TOKEN:
+ * [M, K] of x_dtype, a row for each token. */
+typedef enum { BL_GATE_NONE = 0, BL_GATE_CHANNEL = 1, BL_GATE_TOKEN = 2 } bl_gate;
+
+/* bitlinear_block_norm.
+ *   h        [M, K] h_dtype.
+ *   block    [M, K] x_dtype, or NULL: then h' = h, h_out must be NULL, and
+ *            there is no gate and no norm_post.
+ *   gate     as gate_kind says (NULL for BL_GATE_NONE).
+ *   *_weight, *_bias  [K] p_dtype, or NULL for 1 and 0. eps: finite, > 0.
+ *   h_out    out [M, K] h_dtype: h'; may be h itself (update in place).
+ *   n        out [M, K] x_dtype, or NULL.
+ *   xq, scale  out [M, K] int8 and [M] float, or both NULL: the codes that
+ *            bitlinear_quant_acts gives for n in fp32 (before n's rounding).
+ *   stats    out [M, 4] float, or NULL: post mean, post 1 / deviation, pre
+ *            mean, pre 1 / deviation (0 and 1 without the norm), for the
+ *            backward pass.
+ * norm_pre takes h' before it is rounded to h_dtype. With norm_pre at least
+ * one of n and xq is required; without, both must be NULL. M = 0 is a no-op.
+ * Apart from h and h_out, no output may overlap another argument. */
+bl_status bitlinear_block_norm(const void *h, int h_dtype, const void *block, int x_dtype,
+                               float res_scale, const void *gate, int gate_kind, int post_kind,
+                               const void *post_weight, const void *post_bias, float post_eps,
+                               int pre_kind, const void *pre_weight, const void *pre_bias,
+                               float pre_eps, int p_dtype, int64_t M, int64_t K, void *h_out,
+                               void *n, int8_t *xq, float *scale, float *stats, void *stream);
+
+/* Device workspace (bytes) of bitlinear_block_norm_backward; 0 for an empty or
+ * refused shape. */
+size_t bitlinear_block_norm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* bitlinear_block_norm_backward: gradients of the pass above. (Codes have the
+ * straight-through estimator's gradient: hand the gradient of the quantised
+ * input in as grad_n.)
+ *   grad_h_out [M, K] h_dtype, or NULL (zero): the gradient of h' from its
+ *            other uses (the residual path).
+ *   grad_n   [M, K] gn_dtype; NULL exactly when pre_kind is BL_NORM_NONE.
+ *   h_out    [M, K] h_dtype: h' as the forward pass stored it (h itself
+ *            without a block). block, gate, weights, biases: as in the forward
+ *            pass. stats: its [M, 4].
+ *   grad_h   out [M, K] h_dtype.
+ *   grad_block out [M, K] x_dtype, or NULL (must be NULL without a block).
+ *   grad_gate  out [K] float (channel) or [M, K] x_dtype (token), or NULL.
+ *   grad_*_weight, grad_*_bias  out [K] float, or NULL; each needs its norm.
+ * Row sums are held in fp32 or fp64; column sums are fp32 over at most 512
+ * tokens at a time, added in fp64 in a fixed order, so that results do not
+ * change from run to run. The workspace is always needed (it holds the
+ * column partials and per-row sums). No output may overlap an input. M, K at
+ * most 2^24. M = 0 writes zeros to the [K] outputs. */
+bl_status bitlinear_block_norm_backward(
+    const void *grad_h_out, const void *grad_n, int gn_dtype, const void *h_out, int h_dtype,
+    const void *block, int x_dtype, const float *stats, float res_scale, const void *gate,
+    int gate_kind, int post_kind, const void *post_weight, const void *post_bias, int pre_kind,
+    const void *pre_weight, int p_dtype, int64_t M, int64_t K, void *grad_h, void *grad_block,
+    void *grad_gate, float *grad_post_weight, float *grad_post_bias, float *grad_pre_weight,
+    float *grad_pre_bias, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Dry run of the product dispatch: describes, without launching anything or
  * touching device memory, the kernel launches bitlinear_forward (fused = 0)
  * or bitlinear_linear with bf16 x (fused = 1) would enqueue for an M x N x K

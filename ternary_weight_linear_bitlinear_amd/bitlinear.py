@@ -9,11 +9,18 @@ Functions keep the C names (``bitlinear_pack_weights``,
 ``bitlinear_quant_acts``, ``bitlinear_forward``, ``bitlinear_linear``,
 ``bitlinear_backward_input``, ``bitlinear_backward_weight``) and take torch
 tensors; ``linear`` chains activation quantisation and the forward product.
+
+Around the product: ``bitlinear_forward_epilogue`` / ``bitlinear_linear_epilogue``
+(``linear_epilogue`` picks one) add bias, activation and residual,
+``bitlinear_block_norm`` takes the norms before and after a block with the gate
+and the residual stream between them; each has its backward call.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +31,13 @@ BL_F32, BL_BF16 = 0, 1
 BL_PACK_2BIT, BL_PACK_BASE3, BL_PACK_1BIT = 0, 1, 2
 BL_TERNARY, BL_BINARY = 0, 1
 
+BL_ACT_NONE, BL_ACT_RELU, BL_ACT_RELU2, BL_ACT_SILU, BL_ACT_GELU, BL_ACT_GELU_TANH = range(6)
+BL_NORM_NONE, BL_NORM_RMS, BL_NORM_LAYER = range(3)
+BL_GATE_NONE, BL_GATE_CHANNEL, BL_GATE_TOKEN = range(3)
+
+ACTS = {"none": BL_ACT_NONE, "relu": BL_ACT_RELU, "relu2": BL_ACT_RELU2, "silu": BL_ACT_SILU,
+        "gelu": BL_ACT_GELU, "gelu_tanh": BL_ACT_GELU_TANH}
+NORMS = {"none": BL_NORM_NONE, "rms": BL_NORM_RMS, "layer": BL_NORM_LAYER}
 LAYOUTS = {"2bit": BL_PACK_2BIT, "base3": BL_PACK_BASE3, "1bit": BL_PACK_1BIT}
 SCHEMES = {"ternary": BL_TERNARY, "binary": BL_BINARY}
 _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
@@ -83,6 +97,26 @@ _lib.bitlinear_backward_input.restype = _int
 _lib.bitlinear_backward_input.argtypes = [_p, _int, _p, _int, _p, _i64, _i64, _i64, _p, _p]
 _lib.bitlinear_backward_weight.restype = _int
 _lib.bitlinear_backward_weight.argtypes = [_p, _p, _int, _i64, _i64, _i64, _p, _p]
+_lib.bitlinear_forward_epilogue.restype = _int
+_lib.bitlinear_forward_epilogue.argtypes = [_p, _p, _p, _int, _p, _p, _int, _i64, _i64, _p, _int,
+                                            _int, _p, _f32, _p, _p, _int, _p]
+_lib.bitlinear_linear_epilogue.restype = _int
+_lib.bitlinear_linear_epilogue.argtypes = [_p, _int, _p, _int, _p, _p, _int, _i64, _i64, _p, _int,
+                                           _int, _p, _f32, _p, _p, _int, _p]
+_lib.bitlinear_epilogue_backward_workspace_bytes.restype = _sz
+_lib.bitlinear_epilogue_backward_workspace_bytes.argtypes = [_i64, _i64]
+_lib.bitlinear_epilogue_backward.restype = _int
+_lib.bitlinear_epilogue_backward.argtypes = [_p, _int, _p, _int, _int, _f32, _i64, _i64, _p, _int,
+                                             _p, _p, _p, _sz, _p]
+_lib.bitlinear_block_norm.restype = _int
+_lib.bitlinear_block_norm.argtypes = [_p, _int, _p, _int, _f32, _p, _int, _int, _p, _p, _f32,
+                                      _int, _p, _p, _f32, _int, _i64, _i64, _p, _p, _p, _p, _p, _p]
+_lib.bitlinear_block_norm_backward_workspace_bytes.restype = _sz
+_lib.bitlinear_block_norm_backward_workspace_bytes.argtypes = [_i64, _i64]
+_lib.bitlinear_block_norm_backward.restype = _int
+_lib.bitlinear_block_norm_backward.argtypes = [_p, _p, _int, _p, _int, _p, _int, _p, _f32, _p, _int,
+                                               _int, _p, _p, _int, _p, _int, _i64, _i64, _p, _p,
+                                               _p, _p, _p, _p, _p, _p, _sz, _p]
 _lib.bitlinear_forward_plan.restype = _int
 _lib.bitlinear_forward_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, ctypes.c_char_p, _sz]
 _lib.bitlinear_status_string.restype = ctypes.c_char_p
@@ -95,7 +129,11 @@ EXPORTED = ["bitlinear_packed_row_bytes", "bitlinear_pack_workspace_bytes",
             "bitlinear_pack_noalloc_max_scratch_bytes", "bitlinear_quant_acts", "bitlinear_forward",
             "bitlinear_linear", "bitlinear_forward_segmented", "bitlinear_linear_segmented",
             "bitlinear_forward_lut", "bitlinear_backward_input", "bitlinear_backward_weight",
-            "bitlinear_forward_plan", "bitlinear_status_string", "bitlinear_version",
+            "bitlinear_forward_epilogue", "bitlinear_linear_epilogue",
+            "bitlinear_epilogue_backward_workspace_bytes", "bitlinear_epilogue_backward",
+            "bitlinear_block_norm", "bitlinear_block_norm_backward_workspace_bytes",
+            "bitlinear_block_norm_backward", "bitlinear_forward_plan", "bitlinear_status_string",
+            "bitlinear_version",
             "bitlinear_source_hash"]
 FUSED_MAX_M = 4
 
@@ -358,3 +396,376 @@ def linear(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor, N: int, l
     xq, scale = bitlinear_quant_acts(x, stream=stream)
     return bitlinear_forward(xq, scale, packed, gamma, N, x.shape[1], layout, out_dtype,
                              stream=stream)
+
+
+# ---- bias, activation and residual in the epilogue; norms around a block ----
+# These calls check what the C ABI cannot see (shapes, types, devices, strides)
+# and raise BitLinearError for it as for the library's own refusals. They run on
+# the device of their first tensor and on its current stream unless `stream` is given.
+def _refuse(where: str, why: str):
+    e = BitLinearError(BL_ERR_INVALID_ARG, where)
+    e.args = (f"{e.args[0]}: {why}",)
+    raise e
+
+
+def _take(where: str, name: str, t, shape, dtypes, dev) -> int | None:
+    """Address of a tensor argument (None for None) that must be contiguous, on
+    `dev`, of one of `dtypes` and of this shape."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        _refuse(where, f"{name} is {t.dtype}")
+    if t.shape != shape:
+        _refuse(where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != dev:
+        _refuse(where, f"{name} is on {t.device}, not on {dev}")
+    if not t.is_contiguous():
+        _refuse(where, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+
+
+def _run(where: str, dev: torch.device, stream, call, args) -> None:
+    """One library call on `dev` and its current stream."""
+    if dev.type != "cuda":
+        _refuse(where, f"tensors are on {dev}")
+    if dev.index == torch.cuda.current_device():
+        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None
+                    else stream.cuda_stream), where)
+        return
+    with torch.cuda.device(dev):
+        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None
+                    else stream.cuda_stream), where)
+
+
+def _finite(where: str, name: str, v) -> float:
+    v = float(v)
+    if not math.isfinite(v):
+        _refuse(where, f"{name} is {v}")
+    return v
+
+
+def _one_of(where: str, name: str, v, table) -> int:
+    if isinstance(v, str):
+        if v not in table:
+            _refuse(where, f"{name} is {v!r}, not one of {', '.join(table)}")
+        return table[v]
+    return int(v)
+
+
+def _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act, residual,
+                      residual_scale, out_dtype, y, z, stream):
+    lay = _one_of(where, "layout", layout, LAYOUTS)
+    table, nseg, N = _seg_table((seg_rows,) if isinstance(seg_rows, int) else seg_rows)
+    if out_dtype is None:
+        out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.float32
+    if out_dtype not in _FLOATS:
+        _refuse(where, f"out_dtype is {out_dtype}")
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+    want_z = z is not None and z is not False
+    if z is True:
+        z = torch.empty((M, N), dtype=out_dtype, device=dev)
+    rb = bitlinear_packed_row_bytes(K, lay)
+    own = (out_dtype,)
+    if gammas.numel() < nseg or gammas.dtype != torch.float32 or gammas.device != dev:
+        _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for {nseg} segments")
+    if not gammas.is_contiguous():
+        _refuse(where, "gammas is not contiguous")
+    args = (_take(where, "packed", packed, (N, rb), (torch.uint8,), dev), lay, gammas.data_ptr(), table, nseg,
+            M, K, _take(where, "bias", bias, (N,), _FLOATS, dev),
+            BL_F32 if bias is None else _DTYPES[bias.dtype], _one_of(where, "act", act, ACTS),
+            _take(where, "residual", residual, (M, N), own, dev),
+            _finite(where, "residual_scale", residual_scale),
+            _take(where, "z", z, (M, N), own, dev) if want_z else None,
+            _take(where, "y", y, (M, N), own, dev), _DTYPES[out_dtype])
+    _run(where, dev, stream, getattr(_lib, where), lead + args)
+    return (y, z) if want_z else y
+
+
+def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tensor,
+                               gammas: torch.Tensor, seg_rows, K: int, layout="2bit", bias=None,
+                               act="none", residual=None, residual_scale: float = 1.0,
+                               out_dtype=None, y: torch.Tensor | None = None,
+                               z: torch.Tensor | bool | None = None, stream=None):
+    """y = act(z) + residual_scale * residual with z = the product of
+    bitlinear_forward (bitlinear_forward_segmented) + bias.
+
+    seg_rows: N, or the row counts of stacked matrices (gammas[s] each).
+    residual may be y itself. out_dtype defaults to y's, then residual's type,
+    then fp32; y, z and residual share it. Returns y, or (y, z) when z is
+    requested."""
+    where = "bitlinear_forward_epilogue"
+    if xq.dim() != 2:
+        _refuse(where, f"xq has shape {tuple(xq.shape)}")
+    M, dev = xq.shape[0], xq.device
+    lead = (_take(where, "xq", xq, (M, K), (torch.int8,), dev),
+            _take(where, "scale", scale, (M,), _F32, dev))
+    return _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act,
+                             residual, residual_scale, out_dtype, y, z, stream)
+
+
+def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
+                              layout="2bit", bias=None, act="none", residual=None,
+                              residual_scale: float = 1.0, out_dtype=None,
+                              y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None,
+                              stream=None):
+    """bitlinear_forward_epilogue fused with the quantisation of x, M <= 4 tokens."""
+    where = "bitlinear_linear_epilogue"
+    if x.dim() != 2 or x.dtype not in _FLOATS:
+        _refuse(where, f"x is {x.dtype} of shape {tuple(x.shape)}")
+    (M, K), dev = x.shape, x.device
+    lead = (_take(where, "x", x, (M, K), _FLOATS, dev), _DTYPES[x.dtype])
+    return _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act,
+                             residual, residual_scale, out_dtype, y, z, stream)
+
+
+def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
+                    layout="2bit", bias=None, act="none", residual=None,
+                    residual_scale: float = 1.0, out_dtype=None, y: torch.Tensor | None = None,
+                    z: torch.Tensor | bool | None = None, stream=None):
+    """``linear`` with bias, activation and residual: one fused launch for
+    M <= 4, otherwise quantise then multiply."""
+    more = (layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
+    if x.shape[0] <= FUSED_MAX_M:
+        return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, *more)
+    if x.device.index != torch.cuda.current_device():
+        with torch.cuda.device(x.device):
+            return linear_epilogue(x, packed, gammas, seg_rows, *more)
+    xq, scale = bitlinear_quant_acts(x, stream=stream)
+    return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, x.shape[1], *more)
+
+
+def _workspace(where: str, ws, need: int, dev):
+    if ws is None:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _refuse(where, "workspace is on another device or not contiguous")
+    return ws, ws.numel() * ws.element_size()
+
+
+class EpilogueGrads(NamedTuple):
+    grad_z: torch.Tensor | None
+    grad_bias: torch.Tensor | None
+    grad_residual: torch.Tensor | None
+
+
+def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
+    return int(_lib.bitlinear_epilogue_backward_workspace_bytes(M, N))
+
+
+def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, act="none",
+                                residual_scale: float = 1.0, out_dtype=None,
+                                grad_z: torch.Tensor | bool | None = True,
+                                grad_bias: torch.Tensor | bool | None = True,
+                                grad_residual: torch.Tensor | bool | None = None,
+                                workspace: torch.Tensor | None = None, stream=None) -> EpilogueGrads:
+    """Gradients of y = act(z) + residual_scale * residual, z = product + bias:
+    grad_z [M, N] (out_dtype, grad_y's type by default), grad_bias [N] fp32,
+    grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
+    None (leave out). z may be None for act "none"."""
+    where = "bitlinear_epilogue_backward"
+    if grad_y.dim() != 2 or grad_y.dtype not in _FLOATS:
+        _refuse(where, f"grad_y is {grad_y.dtype} of shape {tuple(grad_y.shape)}")
+    (M, N), dev = grad_y.shape, grad_y.device
+    if out_dtype is None:
+        out_dtype = grad_z.dtype if isinstance(grad_z, torch.Tensor) else grad_y.dtype
+
+    def out(t, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev) if t is True else None if t is False else t
+
+    r = EpilogueGrads(out(grad_z, (M, N), out_dtype), out(grad_bias, (N,), torch.float32),
+                      out(grad_residual, (M, N), grad_y.dtype))
+    need = bitlinear_epilogue_backward_workspace_bytes(M, N) if r.grad_bias is not None else 0
+    ws, ws_bytes = _workspace(where, workspace, need, dev)
+    args = (_take(where, "grad_y", grad_y, (M, N), _FLOATS, dev), _DTYPES[grad_y.dtype],
+            _take(where, "z", z, (M, N), _FLOATS, dev), BL_F32 if z is None else _DTYPES[z.dtype],
+            _one_of(where, "act", act, ACTS), _finite(where, "residual_scale", residual_scale), M, N,
+            _take(where, "grad_z", r.grad_z, (M, N), (out_dtype,), dev),
+            _DTYPES[out_dtype] if out_dtype in _DTYPES else _refuse(where, f"out_dtype is {out_dtype}"),
+            _take(where, "grad_bias", r.grad_bias, (N,), _F32, dev),
+            _take(where, "grad_residual", r.grad_residual, (M, N), (grad_y.dtype,), dev),
+            ws.data_ptr(), ws_bytes)
+    _run(where, dev, stream, _lib.bitlinear_epilogue_backward, args)
+    return r
+
+
+class Norm(NamedTuple):
+    """A norm of bitlinear_block_norm: "rms" or "layer", its [K] weight and bias
+    (None: 1 and 0) and eps."""
+    kind: str | int = "rms"
+    weight: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+    eps: float = 1e-5
+
+
+class BlockNorm(NamedTuple):
+    h_out: torch.Tensor | None
+    n: torch.Tensor | None
+    xq: torch.Tensor | None
+    scale: torch.Tensor | None
+    stats: torch.Tensor | None
+
+
+class BlockNormGrads(NamedTuple):
+    grad_h: torch.Tensor
+    grad_block: torch.Tensor | None
+    grad_gate: torch.Tensor | None
+    grad_post_weight: torch.Tensor | None
+    grad_post_bias: torch.Tensor | None
+    grad_pre_weight: torch.Tensor | None
+    grad_pre_bias: torch.Tensor | None
+
+
+_NO_NORM = Norm(BL_NORM_NONE)
+
+
+def _norm_args(where, M, K, dev, x_dtype, pre, post, gate):
+    """(post kind, weight, bias), (pre kind, weight, bias), p_dtype, (gate, gate_kind)."""
+    post, pre = post or _NO_NORM, pre or _NO_NORM
+    params = [t for t in (post.weight, post.bias, pre.weight, pre.bias) if t is not None]
+    kind = BL_GATE_NONE
+    if gate is not None:
+        kind = BL_GATE_TOKEN if gate.dim() == 2 else BL_GATE_CHANNEL
+        if kind == BL_GATE_CHANNEL:
+            params.append(gate)
+    p_dtype = params[0].dtype if params else torch.float32
+    if p_dtype not in _FLOATS:
+        _refuse(where, f"parameters are {p_dtype}")
+    own, row = (p_dtype,), (K,)
+
+    def side(name, s):
+        return (_one_of(where, f"{name}.kind", s.kind, NORMS),
+                _take(where, f"{name}.weight", s.weight, row, own, dev),
+                _take(where, f"{name}.bias", s.bias, row, own, dev))
+
+    g = _take(where, "gate", gate, (M, K) if kind == BL_GATE_TOKEN else row,
+              (x_dtype,) if kind == BL_GATE_TOKEN else own, dev)
+    return side("post", post), side("pre", pre), _DTYPES[p_dtype], (g, kind)
+
+
+def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
+                         pre: Norm | None = None, post: Norm | None = None,
+                         gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                         out_dtype=None, normed: bool = True, quant: bool = False,
+                         h_out: torch.Tensor | None = None, n: torch.Tensor | None = None,
+                         xq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                         stats: torch.Tensor | bool | None = None, stream=None) -> BlockNorm:
+    """h_out = residual_scale * h + gate * post(block) and n = pre(h_out), in one
+    pass over h [M, K] and block [M, K].
+
+    block None: h_out is h (not written) and only pre runs. gate: [K], or [M, K]
+    of block's type. n has block's type (out_dtype without a block, h's by
+    default); normed=False leaves it out. quant: also the INT8 codes and scale of
+    n, as bitlinear_quant_acts(n in fp32). stats (a buffer or True): what the
+    backward call needs. h_out may be h."""
+    where = "bitlinear_block_norm"
+    if h.dim() != 2 or h.dtype not in _FLOATS:
+        _refuse(where, f"h is {h.dtype} of shape {tuple(h.shape)}")
+    shape, dev = h.shape, h.device
+    M, K = shape
+    x_dtype = block.dtype if block is not None else out_dtype or (n.dtype if n is not None else h.dtype)
+    if x_dtype not in _FLOATS or (out_dtype is not None and out_dtype != x_dtype):
+        _refuse(where, f"block is {x_dtype}, out_dtype {out_dtype}")
+    post_a, pre_a, p_dtype, (g, gate_kind) = _norm_args(where, M, K, dev, x_dtype, pre, post, gate)
+    if block is not None and h_out is None:
+        h_out = torch.empty(shape, dtype=h.dtype, device=dev)
+    if pre is None or not normed:
+        if n is not None:
+            _refuse(where, "n is given without a norm that writes it")
+    elif n is None:
+        n = torch.empty(shape, dtype=x_dtype, device=dev)
+    quant = quant or xq is not None or scale is not None
+    if quant:
+        if xq is None:
+            xq = torch.empty(shape, dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(max(M, 1), dtype=torch.float32, device=dev)[:M]
+    if stats is True:
+        stats = torch.empty((M, 4), dtype=torch.float32, device=dev)
+    elif stats is False:
+        stats = None
+    args = (_take(where, "h", h, shape, _FLOATS, dev), _DTYPES[h.dtype],
+            _take(where, "block", block, shape, _FLOATS, dev), _DTYPES[x_dtype],
+            _finite(where, "residual_scale", residual_scale), g, gate_kind,
+            *post_a, 1.0 if post is None else float(post.eps),
+            *pre_a, 1.0 if pre is None else float(pre.eps), p_dtype, M, K,
+            _take(where, "h_out", h_out, shape, (h.dtype,), dev),
+            _take(where, "n", n, shape, (x_dtype,), dev),
+            _take(where, "xq", xq, shape, (torch.int8,), dev),
+            _take(where, "scale", scale, (M,), _F32, dev),
+            _take(where, "stats", stats, (M, 4), _F32, dev))
+    _run(where, dev, stream, _lib.bitlinear_block_norm, args)
+    return BlockNorm(h if block is None else h_out, n, xq, scale, stats)
+
+
+def bitlinear_block_norm_backward_workspace_bytes(M: int, K: int) -> int:
+    return int(_lib.bitlinear_block_norm_backward_workspace_bytes(M, K))
+
+
+def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch.Tensor | None,
+                                  h_out: torch.Tensor, block: torch.Tensor | None,
+                                  stats: torch.Tensor, pre: Norm | None = None,
+                                  post: Norm | None = None, gate: torch.Tensor | None = None,
+                                  residual_scale: float = 1.0, params: bool = True,
+                                  grad_h: torch.Tensor | None = None,
+                                  grad_block: torch.Tensor | None = None,
+                                  grad_gate: torch.Tensor | None = None,
+                                  grad_post_weight: torch.Tensor | None = None,
+                                  grad_post_bias: torch.Tensor | None = None,
+                                  grad_pre_weight: torch.Tensor | None = None,
+                                  grad_pre_bias: torch.Tensor | None = None,
+                                  workspace: torch.Tensor | None = None,
+                                  stream=None) -> BlockNormGrads:
+    """Gradients of bitlinear_block_norm. h_out, stats: as that call returned
+    them; grad_h_out: the gradient of h_out from its other uses (None: zero);
+    grad_n: the gradient of n (None without pre), or of the quantised input
+    (straight-through). Parameter gradients are fp32 [K] (a gate per token: [M, K]
+    of block's type); params=False leaves out those that no buffer is given for."""
+    where = "bitlinear_block_norm_backward"
+    if h_out.dim() != 2 or h_out.dtype not in _FLOATS:
+        _refuse(where, f"h_out is {h_out.dtype} of shape {tuple(h_out.shape)}")
+    shape, dev = h_out.shape, h_out.device
+    M, K = shape
+    x_dtype = block.dtype if block is not None else h_out.dtype
+    if x_dtype not in _FLOATS:
+        _refuse(where, f"block is {x_dtype}")
+    post_a, pre_a, p_dtype, (g, gate_kind) = _norm_args(where, M, K, dev, x_dtype, pre, post, gate)
+    if grad_h is None:
+        grad_h = torch.empty(shape, dtype=h_out.dtype, device=dev)
+    if grad_block is None and block is not None:
+        grad_block = torch.empty(shape, dtype=x_dtype, device=dev)
+
+    def sums(t, p):
+        return torch.empty(K, dtype=torch.float32, device=dev) if t is None and params and p is not None else t
+
+    if post is not None:
+        grad_post_weight, grad_post_bias = sums(grad_post_weight, post.weight), sums(grad_post_bias, post.bias)
+    if pre is not None:
+        grad_pre_weight, grad_pre_bias = sums(grad_pre_weight, pre.weight), sums(grad_pre_bias, pre.bias)
+    if gate_kind == BL_GATE_CHANNEL:
+        grad_gate = sums(grad_gate, gate)
+    elif gate_kind == BL_GATE_TOKEN and grad_gate is None and params:
+        grad_gate = torch.empty(shape, dtype=x_dtype, device=dev)
+    token = gate_kind == BL_GATE_TOKEN
+    ws, ws_bytes = _workspace(where, workspace, bitlinear_block_norm_backward_workspace_bytes(M, K), dev)
+    args = (_take(where, "grad_h_out", grad_h_out, shape, (h_out.dtype,), dev),
+            _take(where, "grad_n", grad_n, shape, _FLOATS, dev),
+            BL_F32 if grad_n is None else _DTYPES[grad_n.dtype],
+            _take(where, "h_out", h_out, shape, _FLOATS, dev), _DTYPES[h_out.dtype],
+            _take(where, "block", block, shape, _FLOATS, dev), _DTYPES[x_dtype],
+            _take(where, "stats", stats, (M, 4), _F32, dev),
+            _finite(where, "residual_scale", residual_scale), g, gate_kind, *post_a, *pre_a[:2],
+            p_dtype, M, K, _take(where, "grad_h", grad_h, shape, (h_out.dtype,), dev),
+            _take(where, "grad_block", grad_block, shape, (x_dtype,), dev),
+            _take(where, "grad_gate", grad_gate, shape if token else (K,), (x_dtype,) if token else _F32, dev),
+            _take(where, "grad_post_weight", grad_post_weight, (K,), _F32, dev),
+            _take(where, "grad_post_bias", grad_post_bias, (K,), _F32, dev),
+            _take(where, "grad_pre_weight", grad_pre_weight, (K,), _F32, dev),
+            _take(where, "grad_pre_bias", grad_pre_bias, (K,), _F32, dev), ws.data_ptr(), ws_bytes)
+    _run(where, dev, stream, _lib.bitlinear_block_norm_backward, args)
+    return BlockNormGrads(grad_h, grad_block, grad_gate, grad_post_weight, grad_post_bias,
+                          grad_pre_weight, grad_pre_bias)

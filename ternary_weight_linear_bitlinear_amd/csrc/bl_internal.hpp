@@ -167,6 +167,79 @@ hipError_t launch_forward_gemm(const int8_t *xq, const float *scale,
                                int64_t K, void *y, int y_dtype, int32_t *acc,
                                hipStream_t stream);
 
+// ---- products with bias, activation and residual in the epilogue ----------
+// (skinny_epilogue.hip, gemm_epilogue_*.hip); residual and z are typed as y.
+struct EpilogueArgs {
+    const void *bias;  // [N], bias_dtype; NULL = none
+    int bias_dtype;
+    int act;  // kAct* (activation.hpp)
+    const void *residual;
+    float res_scale;
+    void *z;
+};
+hipError_t launch_epilogue_skinny(const int8_t *xq, const float *scale, const uint8_t *packed,
+                                  int layout, const GammaMap &gamma, int64_t M, int64_t N,
+                                  int64_t K, void *y, int y_dtype, const EpilogueArgs &ep,
+                                  hipStream_t stream);
+hipError_t launch_epilogue_linear(const void *x, int x_dtype, const uint8_t *packed, int layout,
+                                  const GammaMap &gamma, int64_t M, int64_t N, int64_t K, void *y,
+                                  int y_dtype, const EpilogueArgs &ep, hipStream_t stream);
+#define BL_EPILOGUE_GEMM(NAME)                                                                    \
+    hipError_t NAME(const int8_t *xq, const float *scale, const uint8_t *packed,                  \
+                    const GammaMap &gamma, int64_t M, int64_t N, int64_t K, void *y, int y_dtype, \
+                    const EpilogueArgs &ep, hipStream_t stream)
+BL_EPILOGUE_GEMM(launch_epilogue_gemm_2bit);
+BL_EPILOGUE_GEMM(launch_epilogue_gemm_base3);
+BL_EPILOGUE_GEMM(launch_epilogue_gemm_1bit);
+#undef BL_EPILOGUE_GEMM
+// Backward of that epilogue (epilogue.hip): grad_z = grad_y * act'(z), the
+// column sums of grad_z, res_scale * grad_y.
+struct EpilogueGradArgs {
+    const void *grad_y, *z;
+    void *grad_z, *grad_residual;
+    float *grad_bias, *workspace;
+    int gy_dtype, z_dtype, gz_dtype, act;
+    float res_scale;
+    int64_t M, N;
+};
+int64_t epilogue_grad_parts(int64_t M, int64_t N);  // partial sums per column in the workspace
+hipError_t launch_epilogue_backward(const EpilogueGradArgs &a, hipStream_t stream);
+
+// ---- norms around a block (norm.hip) --------------------------------------
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
+constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2;
+struct NormSide {
+    const void *weight, *bias;  // [K], p_dtype; NULL = 1 and 0
+    int kind;
+    float eps;
+};
+struct BlockNormArgs {
+    const void *h, *block, *gate;
+    NormSide post, pre;
+    int h_dtype, x_dtype, p_dtype, gate_kind;
+    float res_scale;
+    int64_t M, K;
+    void *h_out, *n;
+    int8_t *xq;
+    float *scale;
+    float *stats;  // [M, 4]: post mean, post 1/deviation, pre mean, pre 1/deviation
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream);
+struct BlockNormGradArgs {
+    const void *grad_h_out, *grad_n, *h_out, *block, *gate;
+    const float *stats;
+    NormSide post, pre;
+    int h_dtype, x_dtype, gn_dtype, p_dtype, gate_kind;
+    float res_scale;
+    int64_t M, K;
+    void *grad_h, *grad_block;
+    void *grad_gate;  // [K] fp32 (channel) or [M, K] x_dtype (token)
+    float *grad_post_weight, *grad_post_bias, *grad_pre_weight, *grad_pre_bias;
+    float *workspace;
+};
+// Floats of workspace that the backward pass needs (0 if no column is summed).
+int64_t block_norm_grad_workspace(int64_t M, int64_t K);
+hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t stream);
 
 // One token against base-3 codes by activation-side lookup tables (lut.hip).
 hipError_t launch_forward_lut(const int8_t *xq, const float *scale, const uint8_t *packed,

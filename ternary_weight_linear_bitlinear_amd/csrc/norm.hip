@@ -1,0 +1,323 @@
+// Norms before and after a block, with the block's gate and the residual
+// stream between them:
+//   p  = norm_post(block)              norm(x) = (x - mu) w / sqrt(var + eps) + bias
+//   h' = res_scale * h + gate * p      (RMS: mu = 0, var = mean x^2)
+//   n  = norm_pre(h')                  as values, as INT8 codes and scale, or both
+// and the backward pass of all of it. Every statistic and sum is held in fp32
+// or fp64; h' enters norm_pre unrounded, whatever type it is stored in.
+#include "bl_internal.hpp"
+#include "device_util.hpp"
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void put(T *p, int64_t i, float v) {
+    if constexpr (sizeof(T) == 4) p[i] = v;
+    else p[i] = (T)f32_to_bf16_rne(v);
+}
+
+// Parameter k of a [K] vector, or `none` without one.
+template <typename PT>
+__device__ __forceinline__ float param(const void *p, int64_t k, float none) {
+    return p ? Elem<PT>::get(static_cast<const PT *>(p), k) : none;
+}
+
+// Sums of a block's threads, the same value in every thread.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double red[kThreads / 64];
+    v = wave_sum(v);
+    __syncthreads();  // the previous sum has been read
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+    __syncthreads();
+    double s = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) s += red[w];
+    return s;
+}
+__device__ __forceinline__ float block_max(float v) {
+    __shared__ float red[kThreads / 64];
+    v = wave_max(v);
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+    __syncthreads();
+    float m = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) m = fmaxf(m, red[w]);
+    return m;
+}
+
+// One row per workgroup, any K: each statistic is a pass over the row (which
+// stays in the caches), the last pass writes. Every element is read and written
+// by one thread, and nothing is written before the last pass, so h_out may be h.
+template <typename HT, typename XT, typename PT>
+__global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNormArgs a) {
+    const int64_t m = blockIdx.x, K = a.K;
+    const HT *h = static_cast<const HT *>(a.h) + m * K;
+    const XT *b = a.block ? static_cast<const XT *>(a.block) + m * K : nullptr;
+    const XT *gt = a.gate_kind == kGateToken ? static_cast<const XT *>(a.gate) + m * K : nullptr;
+    const void *gc = a.gate_kind == kGateChannel ? a.gate : nullptr;
+
+    auto stats_of = [&](const NormSide &s, auto get, float &mean, float &rstd) {
+        mean = 0.f;
+        rstd = 1.f;
+        if (s.kind == kNormNone) return;
+        if (s.kind == kNormLayer) {
+            double t = 0.0;
+            for (int64_t k = threadIdx.x; k < K; k += kThreads) t += (double)get(k);
+            mean = (float)(block_sum(t) / (double)K);
+        }
+        double v = 0.0;
+        for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+            const double d = (double)get(k) - (double)mean;
+            v += d * d;
+        }
+        rstd = 1.0f / sqrtf((float)(block_sum(v) / (double)K) + s.eps);
+    };
+    auto apply = [&](const NormSide &s, float x, int64_t k, float mean, float rstd) {
+        if (s.kind == kNormNone) return x;
+        const float t = (x - mean) * param<PT>(s.weight, k, 1.f) * rstd;
+        return s.bias ? t + param<PT>(s.bias, k, 0.f) : t;
+    };
+
+    float mean_b = 0.f, rstd_b = 1.f, mean_h, rstd_h;
+    if (b) stats_of(a.post, [&](int64_t k) { return Elem<XT>::get(b, k); }, mean_b, rstd_b);
+    auto stream = [&](int64_t k) {  // h'
+        const float hv = Elem<HT>::get(h, k);
+        if (!b) return hv;
+        float p = apply(a.post, Elem<XT>::get(b, k), k, mean_b, rstd_b);
+        if (gt) p *= Elem<XT>::get(gt, k);
+        if (gc) p *= param<PT>(gc, k, 1.f);
+        return __builtin_fmaf(a.res_scale, hv, p);
+    };
+    stats_of(a.pre, stream, mean_h, rstd_h);
+    float s = 1.f, y = 1.f;
+    if (a.xq) {
+        float top = 0.f;
+        for (int64_t k = threadIdx.x; k < K; k += kThreads)
+            top = fmaxf(top, fabsf(apply(a.pre, stream(k), k, mean_h, rstd_h)));
+        s = fmaxf(block_max(top), 1e-6f);
+        y = 1.0f / s;
+    }
+    if (threadIdx.x == 0) {
+        if (a.xq) a.scale[m] = s;
+        if (a.stats)
+            reinterpret_cast<float4 *>(a.stats)[m] = make_float4(mean_b, rstd_b, mean_h, rstd_h);
+    }
+    for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+        const float hv = stream(k);
+        if (a.h_out) put(static_cast<HT *>(a.h_out), m * K + k, hv);
+        const float nv = apply(a.pre, hv, k, mean_h, rstd_h);
+        if (a.n) put(static_cast<XT *>(a.n), m * K + k, nv);
+        if (a.xq) a.xq[m * K + k] = quant1(nv, s, y);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward. With x^ = (x - mu) rs and v the gradient of a norm's output, the
+// gradient of its input is rs (w v - mean(w v) - x^ mean(w v x^)), the first
+// mean for LayerNorm only. Rows first:
+//   d = grad_h' + J_pre^T grad_n;  grad_h = res_scale d;  grad_block = J_post^T (gate d)
+// then the columns: sum_m of grad_n x^_pre, grad_n, (d g) x^_post and d g (g: a
+// gate per token, else 1); a gate per channel factors out of its sums.
+template <typename HT, typename XT, typename NT, typename PT>
+struct GradRow {
+    const BlockNormGradArgs &a;
+    const HT *G, *h;
+    const NT *gn;
+    const XT *b, *gt;
+    float4 st;
+    __device__ GradRow(const BlockNormGradArgs &a_, int64_t m) : a(a_) {
+        const int64_t at = m * a.K;
+        G = a.grad_h_out ? static_cast<const HT *>(a.grad_h_out) + at : nullptr;
+        h = static_cast<const HT *>(a.h_out) + at;
+        gn = a.grad_n ? static_cast<const NT *>(a.grad_n) + at : nullptr;
+        b = a.block ? static_cast<const XT *>(a.block) + at : nullptr;
+        gt = a.gate_kind == kGateToken ? static_cast<const XT *>(a.gate) + at : nullptr;
+        st = reinterpret_cast<const float4 *>(a.stats)[m];
+    }
+    __device__ float grad_n(int64_t k) const { return Elem<NT>::get(gn, k); }
+    __device__ float pre_hat(int64_t k) const { return (Elem<HT>::get(h, k) - st.z) * st.w; }
+    __device__ float post_hat(int64_t k) const { return (Elem<XT>::get(b, k) - st.x) * st.y; }
+    __device__ float d(int64_t k, float c1, float c2) const {
+        float v = G ? Elem<HT>::get(G, k) : 0.f;
+        if (gn) {
+            const float wv = grad_n(k) * param<PT>(a.pre.weight, k, 1.f);
+            v += st.w * (wv - c1 - pre_hat(k) * c2);
+        }
+        return v;
+    }
+    __device__ float gated(float dv, int64_t k) const { return gt ? dv * Elem<XT>::get(gt, k) : dv; }
+};
+
+template <typename HT, typename XT, typename NT, typename PT>
+__global__ __launch_bounds__(kThreads) void block_norm_grad_rows_kernel(const BlockNormGradArgs a) {
+    const int64_t m = blockIdx.x, K = a.K;
+    const GradRow<HT, XT, NT, PT> r(a, m);
+    const void *gc = a.gate_kind == kGateChannel ? a.gate : nullptr;
+    float c1 = 0.f, c2 = 0.f, e1 = 0.f, e2 = 0.f;
+    if (r.gn) {
+        double s1 = 0.0, s2 = 0.0;
+        for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+            const float wv = r.grad_n(k) * param<PT>(a.pre.weight, k, 1.f);
+            s1 += (double)wv;
+            s2 += (double)wv * (double)r.pre_hat(k);
+        }
+        if (a.pre.kind == kNormLayer) c1 = (float)(block_sum(s1) / (double)K);
+        c2 = (float)(block_sum(s2) / (double)K);
+    }
+    if (threadIdx.x == 0)
+        reinterpret_cast<float2 *>(a.workspace)[m] = make_float2(c1, c2);
+    auto into_post = [&](float dv, int64_t k) {  // gradient of norm_post's output, times its weight
+        float u = r.gated(dv, k) * param<PT>(a.post.weight, k, 1.f);
+        return gc ? u * param<PT>(gc, k, 1.f) : u;
+    };
+    if (r.b && a.post.kind != kNormNone) {
+        double s1 = 0.0, s2 = 0.0;
+        for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+            const float u = into_post(r.d(k, c1, c2), k);
+            s1 += (double)u;
+            s2 += (double)u * (double)r.post_hat(k);
+        }
+        if (a.post.kind == kNormLayer) e1 = (float)(block_sum(s1) / (double)K);
+        e2 = (float)(block_sum(s2) / (double)K);
+    }
+    for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+        const float dv = r.d(k, c1, c2);
+        put(static_cast<HT *>(a.grad_h), m * K + k, r.b ? a.res_scale * dv : dv);
+        if (!r.b) continue;
+        const float u = into_post(dv, k);
+        const float hat = r.post_hat(k);
+        if (a.grad_block)
+            put(static_cast<XT *>(a.grad_block), m * K + k,
+                a.post.kind != kNormNone ? r.st.y * (u - e1 - hat * e2) : u);
+        if (r.gt && a.grad_gate) {
+            const float p = hat * param<PT>(a.post.weight, k, 1.f) + param<PT>(a.post.bias, k, 0.f);
+            put(static_cast<XT *>(a.grad_gate), m * K + k, dv * p);
+        }
+    }
+}
+
+// Column sums over the rows of one chunk, in fp32: at most kChunkRows terms,
+// the chunks are then added in fp64 (block_norm_grad_sums_kernel).
+constexpr int kSums = 4;
+constexpr int64_t kChunkRows = 512;
+int64_t grad_chunks(int64_t M, int64_t K) {
+    const int64_t col_blocks = (K + kThreads - 1) / kThreads;
+    int64_t p = 2048 / col_blocks;  // about eight workgroups for each compute unit
+    if (p > (M + 15) / 16) p = (M + 15) / 16;
+    if (p < (M + kChunkRows - 1) / kChunkRows) p = (M + kChunkRows - 1) / kChunkRows;
+    return p < 1 ? 1 : p;
+}
+
+template <typename HT, typename XT, typename NT, typename PT>
+__global__ __launch_bounds__(kThreads) void block_norm_grad_cols_kernel(const BlockNormGradArgs a,
+                                                                        int64_t chunks) {
+    const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (k >= a.K) return;
+    const int64_t m0 = a.M * blockIdx.y / chunks, m1 = a.M * (blockIdx.y + 1) / chunks;
+    float s[kSums] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t m = m0; m < m1; ++m) {
+        const GradRow<HT, XT, NT, PT> r(a, m);
+        const float2 c = reinterpret_cast<const float2 *>(a.workspace)[m];
+        if (r.gn) {
+            const float g = r.grad_n(k);
+            s[0] = __builtin_fmaf(g, r.pre_hat(k), s[0]);
+            s[1] += g;
+        }
+        if (r.b) {
+            const float v = r.gated(r.d(k, c.x, c.y), k);
+            s[2] = __builtin_fmaf(v, r.post_hat(k), s[2]);
+            s[3] += v;
+        }
+    }
+    float *out = a.workspace + 2 * a.M + (int64_t)blockIdx.y * kSums * a.K + k;
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) out[i * a.K] = s[i];
+}
+
+template <typename PT>
+__global__ __launch_bounds__(kThreads) void block_norm_grad_sums_kernel(const BlockNormGradArgs a,
+                                                                        int64_t chunks) {
+    const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (k >= a.K) return;
+    double s[kSums] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t c = 0; c < chunks; ++c)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i)
+            s[i] += (double)a.workspace[2 * a.M + (c * kSums + i) * a.K + k];
+    if (a.grad_pre_weight) a.grad_pre_weight[k] = (float)s[0];
+    if (a.grad_pre_bias) a.grad_pre_bias[k] = (float)s[1];
+    const bool gc = a.gate_kind == kGateChannel;
+    const double g = gc ? (double)param<PT>(a.gate, k, 1.f) : 1.0;
+    if (a.grad_post_weight) a.grad_post_weight[k] = (float)(g * s[2]);
+    if (a.grad_post_bias) a.grad_post_bias[k] = (float)(g * s[3]);
+    if (gc && a.grad_gate)
+        static_cast<float *>(a.grad_gate)[k] =
+            (float)((double)param<PT>(a.post.weight, k, 1.f) * s[2] +
+                    (double)param<PT>(a.post.bias, k, 0.f) * s[3]);
+}
+
+// Calls go(float or uint16_t pointer) by a tensor's type.
+template <typename F>
+hipError_t typed(int dtype, F go) {
+    return dtype == kF32 ? go(static_cast<float *>(nullptr)) : go(static_cast<uint16_t *>(nullptr));
+}
+template <typename T> using Pointee = std::remove_pointer_t<T>;
+
+}  // namespace
+
+hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
+    return typed(a.h_dtype, [&](auto h) {
+        return typed(a.x_dtype, [&](auto x) {
+            return typed(a.p_dtype, [&](auto p) {
+                using HT = Pointee<decltype(h)>;
+                using XT = Pointee<decltype(x)>;
+                using PT = Pointee<decltype(p)>;
+                hipLaunchKernelGGL((block_norm_rows_kernel<HT, XT, PT>), dim3((unsigned)a.M),
+                                   dim3(kThreads), 0, stream, a);
+                return hipGetLastError();
+            });
+        });
+    });
+}
+
+int64_t block_norm_grad_workspace(int64_t M, int64_t K) {
+    return 2 * M + grad_chunks(M, K) * kSums * K;
+}
+
+hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t stream) {
+    const int64_t chunks = grad_chunks(a.M, a.K);
+    const unsigned col_blocks = (unsigned)((a.K + kThreads - 1) / kThreads);
+    const bool cols = a.grad_pre_weight || a.grad_pre_bias || a.grad_post_weight ||
+                      a.grad_post_bias || (a.grad_gate && a.gate_kind == kGateChannel);
+    return typed(a.h_dtype, [&](auto h) {
+        return typed(a.x_dtype, [&](auto x) {
+            return typed(a.gn_dtype, [&](auto n) {
+                return typed(a.p_dtype, [&](auto p) {
+                    using HT = Pointee<decltype(h)>;
+                    using XT = Pointee<decltype(x)>;
+                    using NT = Pointee<decltype(n)>;
+                    using PT = Pointee<decltype(p)>;
+                    if (a.M > 0) {
+                        hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>),
+                                           dim3((unsigned)a.M), dim3(kThreads), 0, stream, a);
+                        hipError_t e = hipGetLastError();
+                        if (e != hipSuccess || !cols) return e;
+                    }
+                    hipLaunchKernelGGL((block_norm_grad_cols_kernel<HT, XT, NT, PT>),
+                                       dim3(col_blocks, (unsigned)chunks), dim3(kThreads), 0,
+                                       stream, a, chunks);
+                    hipError_t e = hipGetLastError();
+                    if (e != hipSuccess) return e;
+                    hipLaunchKernelGGL((block_norm_grad_sums_kernel<PT>), dim3(col_blocks),
+                                       dim3(kThreads), 0, stream, a, chunks);
+                    return hipGetLastError();
+                });
+            });
+        });
+    });
+}
+
+}  // namespace bl
