@@ -50,26 +50,42 @@ __device__ __forceinline__ float half_gauss(float z) {  // exp(-z^2 / 2)
     return __builtin_amdgcn_exp2f(-0.5f * kLog2E * z * z);
 }
 
-// act(z). The switch is uniform over a launch.
-__device__ __forceinline__ float activate(float z, int act) {
+__device__ __forceinline__ float gelu_erf(float z) {
+    // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 on both sides
+    const float x = fabsf(z);
+    return __builtin_fmaf(-0.5f * x, erfc_sqrt2(x, half_gauss(z)), fmaxf(z, 0.0f));
+}
+__device__ __forceinline__ float gelu_tanh(float z) {
+    // z (1 + tanh(u)) / 2 = z sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3)
+    const float u2 = kGeluTanhC * z * __builtin_fmaf(kGeluTanhA * z, z, 1.0f);
+    return z * sigmoid_fast(u2);
+}
+
+// z = act(z) for each element; one branch (uniform over a launch) for all C.
+template <int C>
+__device__ __forceinline__ void activate_all(float (&z)[C], int act) {
     switch (act) {
-        case kActRelu: return fmaxf(z, 0.0f);
-        case kActRelu2: {
-            const float r = fmaxf(z, 0.0f);
-            return r * r;
-        }
-        case kActSilu: return z * sigmoid_fast(z);
-        case kActGelu: {
-            // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 on both sides
-            const float x = fabsf(z);
-            return __builtin_fmaf(-0.5f * x, erfc_sqrt2(x, half_gauss(z)), fmaxf(z, 0.0f));
-        }
-        case kActGeluTanh: {
-            // z (1 + tanh(u)) / 2 = z sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3)
-            const float u2 = kGeluTanhC * z * __builtin_fmaf(kGeluTanhA * z, z, 1.0f);
-            return z * sigmoid_fast(u2);
-        }
-        default: return z;
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) z[e] = fmaxf(z[e], 0.0f);
+            break;
+        case kActRelu2:
+#pragma unroll
+            for (int e = 0; e < C; ++e) z[e] = fmaxf(z[e], 0.0f) * fmaxf(z[e], 0.0f);
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) z[e] = z[e] * sigmoid_fast(z[e]);
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) z[e] = gelu_erf(z[e]);
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int e = 0; e < C; ++e) z[e] = gelu_tanh(z[e]);
+            break;
+        default: break;
     }
 }
 

@@ -55,19 +55,83 @@ struct Epilogue {
                          : static_cast<const float *>(bias)[n];
     }
 
-    // Up to four consecutive outputs n .. n + 3 (those below N) of token m
-    // from their dequantised products v; y, z and residual have row stride ld.
-    __device__ __forceinline__ void store4(const float (&v)[4], int64_t m, int64_t n, int64_t N,
-                                           int64_t ld, YT *y) const {
-        const int64_t at = m * ld + n;
+    // bias of columns n .. n + C - 1 (0 past N, and without a bias)
+    template <int C>
+    __device__ __forceinline__ void load_bias(int64_t n, int64_t N, float (&b)[C]) const {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < C; ++e) b[e] = bias && n + e < N ? bias_at(n + e) : 0.f;
+    }
+    template <int C>
+    __device__ __forceinline__ static void load(const YT *p, float (&v)[C]) {  // C * sizeof(YT) aligned
+        if constexpr (sizeof(YT) == 4) {
+#pragma unroll
+            for (int e = 0; e < C; e += 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(p + e);
+                v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+            }
+        } else {
+            uint32_t w[C / 2];
+            if constexpr (C == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(p);
+            else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+            for (int e = 0; e < C; e += 2) {
+                v[e] = __uint_as_float(w[e / 2] << 16);
+                v[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
+            }
+        }
+    }
+    template <int C>
+    __device__ __forceinline__ static void store(YT *p, const float (&v)[C]) {
+        if constexpr (sizeof(YT) == 4) {
+#pragma unroll
+            for (int e = 0; e < C; e += 4)
+                *reinterpret_cast<float4 *>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else {
+            uint32_t w[C / 2];
+#pragma unroll
+            for (int e = 0; e < C; e += 2) {
+                const bf16x2 q = {(__bf16)v[e], (__bf16)v[e + 1]};
+                w[e / 2] = __builtin_bit_cast(uint32_t, q);
+            }
+            if constexpr (C == 8) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(w);
+            else *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(w);
+        }
+    }
+
+    // C consecutive outputs n .. n + C - 1 (those below N) of one token from
+    // their dequantised products v; `at` = the token's row offset + n in y, z
+    // and residual. vec: all C are below N and at * sizeof(YT) is aligned to
+    // C outputs.
+    template <int C>
+    __device__ __forceinline__ void finish(float (&v)[C], const float (&b)[C], int64_t at, int64_t n,
+                                           int64_t N, bool vec, YT *y) const {
+        if (bias) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] += b[e];
+        }
+        if (vec) {
+            float r[C];
+            if (residual) load(residual + at, r);
+            if (z) store(z + at, v);
+            activate_all(v, act);
+            if (residual) {
+#pragma unroll
+                for (int e = 0; e < C; ++e) v[e] = __builtin_fmaf(res_scale, r[e], v[e]);
+            }
+            store(y + at, v);
+            return;
+        }
+        if (z) {
+#pragma unroll
+            for (int e = 0; e < C; ++e)
+                if (n + e < N) z[at + e] = narrow(v[e]);
+        }
+        activate_all(v, act);
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
             if (n + e >= N) continue;
-            const float zv = bias ? v[e] + bias_at(n + e) : v[e];
-            float a = activate(zv, act);
-            if (residual) a = __builtin_fmaf(res_scale, widen(residual[at + e]), a);
-            if (z) z[at + e] = narrow(zv);
-            y[at + e] = narrow(a);
+            if (residual) v[e] = __builtin_fmaf(res_scale, widen(residual[at + e]), v[e]);
+            y[at + e] = narrow(v[e]);
         }
     }
 #endif

@@ -83,6 +83,13 @@ struct GemmCfg {
     static constexpr int OUT = (BM / WM) * (BN * 2 + 16);
     static constexpr int SMEM0 = STAGES > RED ? STAGES : RED;
     static constexpr int SMEM = LUT + (SMEM0 > OUT ? SMEM0 : OUT);
+    // The extended epilogue stages INT32 fragment rows (32 x BN) in the same
+    // memory: as many at a time as fit, one at least.
+    static constexpr int kFragRow = 32 * BN * 4;
+    template <typename E>
+    static constexpr int kEpiFrags = SMEM - LUT >= kFragRow ? (SMEM - LUT) / kFragRow : 1;
+    template <typename E>
+    static constexpr int kSmem = E::kActive && SMEM - LUT < kFragRow ? LUT + kFragRow : SMEM;
     static_assert(DIST == 1 || DIST == 2 || DIST == 4, "register sets: 1, 2 or 4");
 };
 
@@ -178,6 +185,77 @@ __device__ __forceinline__ int xcd_tile(int b, int ntiles) {
     const int t = (b % kXcds) * per_xcd + b / kXcds;
     return t < ntiles ? t : -1;
 }
+
+// Extended epilogue of a tile: the INT32 sums go through LDS one fragment row
+// (32 tokens x BN columns) at a time, so that each thread finishes eight
+// consecutive columns of one token and every access to y, z and the residual
+// is a 16-byte (fp32: 32-byte) piece of a whole row. Sums rather than rounded
+// values are staged: everything after them is fp32. Straight from the matrix
+// cores' layout (8-byte pieces scattered over 32 rows) 2048 x 11008 x 4096 with
+// bias, gelu and z took 237 us.
+//
+// LDS slot of 16-byte chunk c of row r: c ^ r within the row, which spreads the
+// 32 rows that a fragment's registers are written to over the banks and keeps a
+// row's chunks one contiguous permutation for the reads.
+template <int BN>
+__device__ __forceinline__ int frag_slot(int row, int chunk) {
+    return (row * (BN / 4) + (chunk ^ row)) * 16;
+}
+template <int BN>
+__device__ __forceinline__ void stage_fragment(int8_t *buf, const v16i &a, int col, int frow, int lg) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<v4i *>(buf + frag_slot<BN>(frow, col / 4 + 2 * q + lg)) =
+            v4i{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+}
+// T threads; a thread keeps its eight columns (and their bias and gammas) over all rows.
+template <int BN, int T, typename YT, typename E>
+struct RowEpilogue {
+    static constexpr int kPieces = BN / 8, kStep = T / kPieces;  // pieces a row, rows a step
+    static_assert(T % kPieces == 0 && 32 % kStep == 0, "whole rows a step");
+    const E &ep;
+    const float *scale;
+    const bool one;
+    const int64_t m0, n, M, N, ld;
+    YT *y;
+    bool vec;
+    int row0, piece;
+    float g0, gam[8], bias[8];
+    __device__ __forceinline__ RowEpilogue(const E &ep_, const GammaMap &gm,
+                                           const float (&gs)[kMaxSegments], const float *scale_,
+                                           int64_t m0_, int64_t n0, int64_t M_, int64_t N_,
+                                           int64_t ld_, YT *y_)
+        : ep(ep_), scale(scale_), one(gm.nseg == 1), m0(m0_), n(n0 + (threadIdx.x % kPieces) * 8),
+          M(M_), N(N_), ld(ld_), y(y_) {
+        row0 = threadIdx.x / kPieces;
+        piece = threadIdx.x % kPieces;
+        vec = n + 8 <= N && ld % (16 / (int)sizeof(YT)) == 0;
+        g0 = gs[0];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gam[e] = one ? g0 : seg_gamma(gm, gs, n + e);
+        ep.load_bias(n, N, bias);
+    }
+    // 32 staged rows, tokens m0 + first ..
+    __device__ __forceinline__ void run(const int8_t *buf, int first) const {
+        if (n >= N) return;
+#pragma unroll 2
+        for (int r = row0; r < 32; r += kStep) {
+            const int64_t m = m0 + first + r;
+            if (m >= M) return;
+            const v4i lo = *reinterpret_cast<const v4i *>(buf + frag_slot<BN>(r, 2 * piece));
+            const v4i hi = *reinterpret_cast<const v4i *>(buf + frag_slot<BN>(r, 2 * piece + 1));
+            const float sm = scale[m];
+            // the factors of the plain epilogue: gamma * scale / 127 for one
+            // matrix, gamma * (scale / 127) for a row of a stack
+            const float f1 = g0 * sm / 127.0f, s127 = sm / 127.0f;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]) * (one ? f1 : gam[e] * s127);
+            ep.finish(v, bias, m * ld + n, n, N, vec, y);
+        }
+    }
+};
 
 template <int LAYOUT, int BM, int BN, int WM, int WN, int DIST, int KG, int KMODE,
           typename YT, typename E>
@@ -499,8 +577,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
                     for (int r = 0; r < 16; ++r) dst[((i * C::FJ + j) * 16 + r) * 64] = acc[i][j][r];
         }
         lds_barrier();
-        if (kg > 0) return;
-        for (int h = 1; h < KG; ++h) {
+        if constexpr (!E::kActive) {
+            if (kg > 0) return;
+        }
+        for (int h = 1; h < (kg > 0 ? 1 : KG); ++h) {
             const int32_t *src = red + ((h - 1) * (WM * WN) + wave) * kRegs * 64 + lane;
 #pragma unroll
             for (int i = 0; i < C::FI; ++i)
@@ -520,6 +600,29 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     float gs[kMaxSegments];
     load_gammas(gm, gs);
     const bool one = gm.nseg == 1;
+    if constexpr (E::kActive) {
+        static_assert(WM == 1, "a fragment row is staged by one row of waves");
+        constexpr int FP = C::template kEpiFrags<E>;  // fragment rows staged at a time
+        const RowEpilogue<BN, kThreads, YT, E> rows(ep, gm, gs, scale, m0, n0, M, N, ldy, y);
+        if constexpr (KG > 1) lds_barrier();  // the other groups' sums have been read
+#pragma unroll
+        for (int i0 = 0; i0 < C::FI; i0 += FP) {
+#pragma unroll
+            for (int i = i0; i < i0 + FP && i < C::FI; ++i) {
+                if (KG > 1 && kg > 0) break;
+                int8_t *buf = reinterpret_cast<int8_t *>(smem + C::LUT) + (i - i0) * 32 * BN * 4;
+#pragma unroll
+                for (int j = 0; j < C::FJ; ++j)
+                    stage_fragment<BN>(buf, acc[i][j], wn * (BN / WN) + j * 32, frow, lg);
+            }
+            lds_barrier();
+#pragma unroll
+            for (int i = i0; i < i0 + FP && i < C::FI; ++i)
+                rows.run(reinterpret_cast<const int8_t *>(smem + C::LUT) + (i - i0) * 32 * BN * 4, 32 * i);
+            if (i0 + FP < C::FI) lds_barrier();  // the next rows reuse the memory
+        }
+        return;
+    }
     const bool full = m0 + BM <= M && n0 + BN <= N && (ldy % 4) == 0;
     if constexpr (!E::kActive && sizeof(YT) == 2 && KG == 1 && BN >= 128) {
         if (full && one && (ldy % 8) == 0) {
@@ -594,13 +697,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
                 }
                 const float v0 = (float)a0 * f[0], v1 = (float)a1 * f[1];
                 const float v2 = (float)a2 * f[2], v3 = (float)a3 * f[3];
-                if constexpr (E::kActive) {
-                    if (m < M) {
-                        const float vv[4] = {v0, v1, v2, v3};
-                        ep.store4(vv, m, n, N, ldy, y);
-                    }
-                    continue;
-                }
                 if (full) {
                     if constexpr (sizeof(YT) == 4) {
                         *reinterpret_cast<float4 *>(y + m * ldy + n) = make_float4(v0, v1, v2, v3);
@@ -817,6 +913,29 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
         step(dma_s1, breg[1], [&]() { load_a(kt + 3, dma_s0); load_w(kt + 3, breg[0]); });
     __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no direct-to-LDS load outlives the block
 
+    if constexpr (E::kActive) {
+        // four fragment rows at a time, one in each array; the barrier keeps
+        // them clear of other waves' direct-to-LDS loads, which each wave has
+        // waited for above
+        lds_barrier();
+        float gse[kMaxSegments];
+        load_gammas(gm, gse);
+        const RowEpilogue<256, 512, YT, E> rows(ep, gm, gse, scale, m0, n0, M, g.N, ldy, y);
+        int8_t *const bufs[4] = {dma_s0, dma_s1, dma_s2, reinterpret_cast<int8_t *>(dma_out)};
+        static_assert(kDmaStage == 32 * 256 * 4 && 64 * kDmaOutRow >= kDmaStage, "a fragment row fits");
+#pragma unroll
+        for (int i0 = 0; i0 < FI; i0 += 4) {
+#pragma unroll
+            for (int i = i0; i < i0 + 4 && i < FI; ++i)
+                stage_fragment<256>(bufs[i - i0], acc[i], wave * 32, frow, lg);
+            lds_barrier();
+#pragma unroll
+            for (int i = i0; i < i0 + 4 && i < FI; ++i) rows.run(bufs[i - i0], 32 * i);
+            if (i0 + 4 < FI) lds_barrier();
+        }
+        return;
+    }
+
     // Epilogue: y = acc * f as bf16; one matrix: f = gamma * scale[m] / 127;
     // stacked segments (SEG): f = gamma(n) * (scale[m] / 127). Rows 64 p ..
     // 64 p + 63 (fragments 2 p and 2 p + 1 of every wave) per pass. (A single
@@ -845,14 +964,6 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e] = seg_gamma(gm, gs, n0 + nl + e) * sm127;
                 }
-                if constexpr (E::kActive) {
-                    if (m < M) {
-                        const float vv[4] = {(float)a0 * f[0], (float)a1 * f[1], (float)a2 * f[2],
-                                             (float)a3 * f[3]};
-                        ep.store4(vv, m, n0 + nl, g.N, ldy, y);
-                    }
-                    continue;
-                }
                 const bf16x2 lo = {(__bf16)((float)a0 * f[0]), (__bf16)((float)a1 * f[1])};
                 const bf16x2 hi = {(__bf16)((float)a2 * f[2]), (__bf16)((float)a3 * f[3])};
                 *reinterpret_cast<uint2 *>(dma_out + (ii * 32 + frow) * kDmaOutRow + nl * 2) =
@@ -861,7 +972,6 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
                     *reinterpret_cast<int4 *>(acc_out + m * ldy + n0 + nl) = make_int4(a0, a1, a2, a3);
             }
         }
-        if constexpr (E::kActive) continue;
         lds_barrier();
         const int rows = FI - 2 * p >= 2 ? 64 : 32;
         for (int c = tid; c < rows * 32; c += 512) {  // 16-byte pieces of the pass's rows
@@ -1055,10 +1165,11 @@ hipError_t launch_gemm_tile(const int8_t *xq, const float *scale, const uint8_t 
     // (128 x 64 tiles keep row order: banded, they measured 2-4% slower)
     g.band = BM == 128 && BN == 64 ? 1 : tile_band(tm, tn, (int64_t)BM * K, (int64_t)BN * rb);
     auto launch = [&](auto kern, LdsFlag *flag) {
-        hipError_t e = allow_dynamic_lds(kern, C::SMEM, flag);
+        hipError_t e = allow_dynamic_lds(kern, C::template kSmem<E>, flag);
         if (e != hipSuccess) return e;
         if constexpr (E::kActive)
-            hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::kThreads), C::SMEM, s, g, ep);
+            hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::kThreads), C::template kSmem<E>,
+                               s, g, ep);
         else
             hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::kThreads), C::SMEM, s, g);
         return hipGetLastError();

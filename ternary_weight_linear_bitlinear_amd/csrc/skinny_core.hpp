@@ -204,11 +204,12 @@ __device__ __forceinline__ void store_epilogue(const GammaMap &gm,
                                                const float (&gs)[kMaxSegments], float scale,
                                                const v4i tot, int64_t m, int64_t n, int64_t N,
                                                YT *y, const Epilogue<YT> &ep) {
-    float f[4];
+    float f[4], bias[4];
     row_factors(gm, gs, scale, n, f);
-    const float v[4] = {(float)tot[0] * f[0], (float)tot[1] * f[1], (float)tot[2] * f[2],
-                        (float)tot[3] * f[3]};
-    ep.store4(v, m, n, N, N, y);
+    ep.load_bias(n, N, bias);
+    float v[4] = {(float)tot[0] * f[0], (float)tot[1] * f[1], (float)tot[2] * f[2],
+                  (float)tot[3] * f[3]};
+    ep.finish(v, bias, m * N + n, n, N, N % 4 == 0 && n + 4 <= N, y);
 }
 
 // RG row groups of 16 weight rows per workgroup share every activation read
