@@ -51,6 +51,33 @@ __device__ __forceinline__ void load8(const uint16_t *p, float v[8]) {
     }
 }
 
+// Eight consecutive elements as loaded (one 16-byte piece of bf16, two of
+// fp32), widened to fp32 only after every load of the thread is in flight.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
+    uint4 a;
+    __device__ __forceinline__ void load(const uint16_t *p) { a = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void widen(float v[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void widen(float v[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+
 // One activation code: q = clamp(rint((x / s) * 127), -127, 127), division,
 // then the multiply, then round half to even, in the order the pages write it
 // ([b158] §3.2 and §5.2). The quotient is formed with Markstein's correction
@@ -150,6 +177,32 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
     return v;
+}
+
+// Wave-wide reductions by lane permutes inside the vector unit (row shifts, then
+// the two row broadcasts; no LDS round trips), the result in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+    v += dpp_or_zero<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8: lane 15 of a row has its sum
+    v += dpp_or_zero<0x112, 0xf>(v);
+    v += dpp_or_zero<0x114, 0xf>(v);
+    v += dpp_or_zero<0x118, 0xf>(v);
+    v += dpp_or_zero<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+    v += dpp_or_zero<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_max0_dpp(float v) {  // of values >= 0
+    v = fmaxf(v, dpp_or_zero<0x111, 0xf>(v));
+    v = fmaxf(v, dpp_or_zero<0x112, 0xf>(v));
+    v = fmaxf(v, dpp_or_zero<0x114, 0xf>(v));
+    v = fmaxf(v, dpp_or_zero<0x118, 0xf>(v));
+    v = fmaxf(v, dpp_or_zero<0x142, 0xa>(v));
+    v = fmaxf(v, dpp_or_zero<0x143, 0xc>(v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // Expand one 32-bit word of the 2-bit layout (16 codes) into four dwords of

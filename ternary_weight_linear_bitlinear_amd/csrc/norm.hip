@@ -8,6 +8,8 @@
 #include "bl_internal.hpp"
 #include "device_util.hpp"
 
+#include <type_traits>
+
 namespace bl {
 namespace {
 
@@ -48,7 +50,268 @@ __device__ __forceinline__ float block_max(float v) {
     return m;
 }
 
-// One row per workgroup, any K: each statistic is a pass over the row (which
+// ---------------------------------------------------------------------------
+// Forward, rows that holds_row() accepts: one workgroup per row, the row held in registers
+// from its one read to its one write. Memory-bound; @@FWD@@
+//
+// Thread t owns J chunks of eight consecutive elements (chunks t, t + T, ...),
+// or, where K % 8 leaves rows unaligned, 8 J single elements T apart (VEC =
+// false). Every load of the row is issued before the first reduction. A
+// statistic is a sum in fp32 over at most 8 J elements of a thread, a wave's 64
+// lanes and 16 waves, so at most 8 J + 22 additions follow one another.
+constexpr int kMaxWaves = 16;
+constexpr int64_t kRegElems = 8 * 64 * kMaxWaves;  // of a row, for each chunk per thread
+// Four chunks fit the registers in vector form only (single elements spill), so
+// unaligned rows past two go through the row's passes instead.
+inline bool holds_row(int64_t K) { return K <= (K % 8 == 0 ? 4 : 2) * kRegElems; }
+
+// Sum (or maximum of values >= 0) over the workgroup; `red` is this reduction's
+// own, so one barrier is enough.
+__device__ __forceinline__ float group_sum(float v, float *red, int waves) {
+    v = wave_sum_dpp(v);
+    if (waves == 1) return v;
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+    lds_barrier();
+    float s = red[0];
+    for (int w = 1; w < waves; ++w) s += red[w];
+    return s;
+}
+__device__ __forceinline__ float group_max0(float v, float *red, int waves) {
+    v = wave_max0_dpp(v);
+    if (waves == 1) return v;
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+    lds_barrier();
+    float s = red[0];
+    for (int w = 1; w < waves; ++w) s = fmaxf(s, red[w]);
+    return s;
+}
+
+// One thread's share of a row: chunk j, element e is element index(j, e) of the
+// row, below K where valid.
+template <int J, bool VEC>
+struct Share {
+    int K, tid, T;
+    __device__ __forceinline__ int index(int j, int e) const {
+        return VEC ? (j * T + tid) * 8 + e : (j * 8 + e) * T + tid;
+    }
+    __device__ __forceinline__ bool valid(int j, int e) const { return index(j, e) < K; }
+};
+// A share of a tensor's row as loaded; elements past K read a valid address and
+// are zeroed when widened.
+template <typename T, int J, bool VEC> struct RowRegs;
+template <typename T, int J> struct RowRegs<T, J, true> {
+    Raw8<T> raw[J];
+    __device__ __forceinline__ void load(const T *row, const Share<J, true> &sh) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) raw[j].load(row + (sh.valid(j, 0) ? sh.index(j, 0) : 0));
+    }
+    __device__ __forceinline__ void widen(int j, const Share<J, true> &sh, float (&v)[8]) const {
+        raw[j].widen(v);
+        const bool ok = sh.valid(j, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ok ? v[e] : 0.f;
+    }
+};
+template <typename T, int J> struct RowRegs<T, J, false> {
+    T raw[J][8];
+    __device__ __forceinline__ void load(const T *row, const Share<J, false> &sh) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) raw[j][e] = row[sh.valid(j, e) ? sh.index(j, e) : 0];
+    }
+    __device__ __forceinline__ void widen(int j, const Share<J, false> &sh, float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sh.valid(j, e) ? Elem<T>::get(&raw[j][e], 0) : 0.f;
+    }
+};
+template <typename T, int J, bool VEC>
+__device__ __forceinline__ void store_share(T *row, int j, const Share<J, VEC> &sh, const float (&v)[8]) {
+    if constexpr (VEC) {
+        if (!sh.valid(j, 0)) return;
+        T *p = row + sh.index(j, 0);
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bf16x2 q = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+                w[i] = __builtin_bit_cast(uint32_t, q);
+            }
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (sh.valid(j, e)) put(row, sh.index(j, e), v[e]);
+    }
+}
+// Chunk j of a [K] parameter vector in fp32: zero past K, ones without the vector.
+template <typename PT, int J, bool VEC>
+__device__ __forceinline__ void load_param(const void *p, int j, const Share<J, VEC> &sh, float (&w)[8]) {
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        return;
+    }
+    const PT *q = static_cast<const PT *>(p);
+    if constexpr (VEC) {
+        Raw8<PT> r;
+        r.load(q + (sh.valid(j, 0) ? sh.index(j, 0) : 0));
+        r.widen(w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = Elem<PT>::get(q, sh.valid(j, e) ? sh.index(j, e) : 0);
+    }
+}
+// The same times a second vector.
+template <typename PT, int J, bool VEC>
+__device__ __forceinline__ void load_params(const void *p, const void *q, int j,
+                                            const Share<J, VEC> &sh, float (&w)[8]) {
+    load_param<PT>(p, j, sh, w);
+    if (!q) return;
+    float f[8];
+    load_param<PT>(q, j, sh, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= f[e];
+}
+
+template <typename HT, typename XT, typename PT, int J, bool VEC>
+__global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockNormArgs a) {
+    __shared__ float red[5][kMaxWaves];
+    const int64_t m = blockIdx.x, K = a.K;
+    const int waves = blockDim.x / 64;
+    const Share<J, VEC> sh{(int)K, (int)threadIdx.x, (int)blockDim.x};
+    const float inv_k = 1.0f / (float)K;
+    const bool block = a.block != nullptr, token = a.gate_kind == kGateToken;
+    const void *gc = a.gate_kind == kGateChannel ? a.gate : nullptr;
+
+    RowRegs<XT, J, VEC> rb, rg;
+    RowRegs<HT, J, VEC> rh;
+    if (block) rb.load(static_cast<const XT *>(a.block) + m * K, sh);
+    rh.load(static_cast<const HT *>(a.h) + m * K, sh);
+    if (token) rg.load(static_cast<const XT *>(a.gate) + m * K, sh);
+    // norm_post's weight and a gate per channel act as one factor. With one
+    // chunk per thread the parameters are fetched along with the row; with more
+    // they would spill, and come (from L2) where they are used.
+    constexpr bool kEarly = J == 1;
+    float wp[8], wn[8];
+    if constexpr (kEarly) {
+        load_params<PT>(a.post.weight, gc, 0, sh, wp);
+        load_param<PT>(a.pre.weight, 0, sh, wn);
+    }
+
+    // mean and 1 / deviation of the share x (zero past K)
+    auto stats_of = [&](const NormSide &s, const float (&x)[J][8], float *red0, float *red1, float &mean,
+                        float &rstd) {
+        mean = 0.f;
+        rstd = 1.f;
+        if (s.kind == kNormNone) return;
+        float t = 0.f;
+        if (s.kind == kNormLayer) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t += x[j][e];
+            mean = group_sum(t, red0, waves) * inv_k;
+            t = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = sh.valid(j, e) ? x[j][e] - mean : 0.f;
+                t = __builtin_fmaf(d, d, t);
+            }
+        rstd = 1.0f / sqrtf(group_sum(t, red1, waves) * inv_k + s.eps);
+    };
+
+    float v[J][8];  // h'
+    float mean_b = 0.f, rstd_b = 1.f, mean_h, rstd_h;
+#pragma unroll
+    for (int j = 0; j < J; ++j) rh.widen(j, sh, v[j]);
+    if (block) {
+        float b[J][8];
+#pragma unroll
+        for (int j = 0; j < J; ++j) rb.widen(j, sh, b[j]);
+        stats_of(a.post, b, red[0], red[1], mean_b, rstd_b);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if constexpr (!kEarly) load_params<PT>(a.post.weight, gc, j, sh, wp);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[j][e] = (b[j][e] - mean_b) * wp[e] * rstd_b;
+            if (a.post.bias) {
+                float pb[8];
+                load_params<PT>(a.post.bias, gc, j, sh, pb);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[j][e] += pb[e];
+            }
+            if (token) {
+                float g[8];
+                rg.widen(j, sh, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[j][e] *= g[e];
+            }
+        }
+        HT *out = static_cast<HT *>(a.h_out) + m * K;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[j][e] = sh.valid(j, e) ? __builtin_fmaf(a.res_scale, v[j][e], b[j][e]) : 0.f;
+            store_share(out, j, sh, v[j]);
+        }
+    }
+    stats_of(a.pre, v, red[2], red[3], mean_h, rstd_h);
+    if (a.stats && threadIdx.x == 0)
+        reinterpret_cast<float4 *>(a.stats)[m] = make_float4(mean_b, rstd_b, mean_h, rstd_h);
+    if (a.pre.kind == kNormNone) return;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        if constexpr (!kEarly) load_param<PT>(a.pre.weight, j, sh, wn);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = (v[j][e] - mean_h) * wn[e] * rstd_h;
+        if (a.pre.bias) {
+            float pb[8];
+            load_param<PT>(a.pre.bias, j, sh, pb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] += pb[e];
+        }
+    }
+    if (a.n) {
+        XT *out = static_cast<XT *>(a.n) + m * K;
+#pragma unroll
+        for (int j = 0; j < J; ++j) store_share(out, j, sh, v[j]);
+    }
+    if (a.xq) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, sh.valid(j, e) ? fabsf(v[j][e]) : 0.f);
+        const float s = fmaxf(group_max0(top, red[4], waves), 1e-6f);
+        const float y = 1.0f / s;
+        if (threadIdx.x == 0) a.scale[m] = s;
+        int8_t *out = a.xq + m * K;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if constexpr (VEC) {
+                if (sh.valid(j, 0))
+                    *reinterpret_cast<uint2 *>(out + sh.index(j, 0)) =
+                        make_uint2(quant4(v[j][0], v[j][1], v[j][2], v[j][3], s, y),
+                                   quant4(v[j][4], v[j][5], v[j][6], v[j][7], s, y));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (sh.valid(j, e)) out[sh.index(j, e)] = quant1(v[j][e], s, y);
+            }
+        }
+    }
+}
+
+// Longer rows: one row per workgroup, any K: each statistic is a pass over the row (which
 // stays in the caches), the last pass writes. Every element is read and written
 // by one thread, and nothing is written before the last pass, so h_out may be h.
 template <typename HT, typename XT, typename PT>
@@ -275,9 +538,26 @@ hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
                 using HT = Pointee<decltype(h)>;
                 using XT = Pointee<decltype(x)>;
                 using PT = Pointee<decltype(p)>;
-                hipLaunchKernelGGL((block_norm_rows_kernel<HT, XT, PT>), dim3((unsigned)a.M),
-                                   dim3(kThreads), 0, stream, a);
-                return hipGetLastError();
+                const dim3 grid((unsigned)a.M);
+                if (!holds_row(a.K)) {
+                    hipLaunchKernelGGL((block_norm_rows_kernel<HT, XT, PT>), grid, dim3(kThreads),
+                                       0, stream, a);
+                    return hipGetLastError();
+                }
+                auto go = [&](auto j_c, auto vec_c) {
+                    constexpr int J = decltype(j_c)::value;
+                    const int64_t threads = ((a.K + 8 * J - 1) / (8 * J) + 63) / 64 * 64;
+                    hipLaunchKernelGGL((block_norm_kernel<HT, XT, PT, J, decltype(vec_c)::value>),
+                                       grid, dim3((unsigned)threads), 0, stream, a);
+                    return hipGetLastError();
+                };
+                auto chunks = [&](auto vec_c) {
+                    if (a.K <= kRegElems) return go(std::integral_constant<int, 1>{}, vec_c);
+                    if constexpr (decltype(vec_c)::value)
+                        if (a.K > 2 * kRegElems) return go(std::integral_constant<int, 4>{}, vec_c);
+                    return go(std::integral_constant<int, 2>{}, vec_c);
+                };
+                return a.K % 8 == 0 ? chunks(std::true_type{}) : chunks(std::false_type{});
             });
         });
     });

@@ -263,33 +263,6 @@ __device__ __forceinline__ float block_max(float v) {
     return r;
 }
 
-// Eight consecutive elements as loaded (one 16-byte piece of bf16, two of
-// fp32), widened to fp32 only after every load of the thread is in flight.
-template <typename T> struct Raw8;
-template <> struct Raw8<uint16_t> {
-    uint4 a;
-    __device__ __forceinline__ void load(const uint16_t *p) { a = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void widen(float v[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-};
-template <> struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = *reinterpret_cast<const float4 *>(p);
-        b = *reinterpret_cast<const float4 *>(p + 4);
-    }
-    __device__ __forceinline__ void widen(float v[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
-
 template <typename T, int J>
 __global__ __launch_bounds__(kThreads) void quant_acts_kernel(
     const T *__restrict__ x, int64_t M, int64_t K, int8_t *__restrict__ xq,
