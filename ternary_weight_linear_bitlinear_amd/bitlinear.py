@@ -18,7 +18,7 @@ and the residual stream between them; each has its backward call.
 from __future__ import annotations
 
 import ctypes
-import math
+import functools
 import os
 from typing import NamedTuple
 
@@ -401,88 +401,113 @@ def linear(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor, N: int, l
 # ---- bias, activation and residual in the epilogue; norms around a block ----
 # These calls check what the C ABI cannot see (shapes, types, devices, strides)
 # and raise BitLinearError for it as for the library's own refusals. They run on
-# the device of their first tensor and on its current stream unless `stream` is given.
+# the device of their first tensor and on its current stream unless `stream` is
+# given. The decode products take a few microseconds, so the checks are kept to
+# one pass over each tensor's attributes and what depends on sizes alone is cached.
+_f32, _bf16 = torch.float32, torch.bfloat16
+_FLT_MAX = 3.4028234663852886e38
+
+
 def _refuse(where: str, why: str):
     e = BitLinearError(BL_ERR_INVALID_ARG, where)
     e.args = (f"{e.args[0]}: {why}",)
     raise e
 
 
-def _take(where: str, name: str, t, shape, dtypes, dev) -> int | None:
-    """Address of a tensor argument (None for None) that must be contiguous, on
-    `dev`, of one of `dtypes` and of this shape."""
-    if t is None:
-        return None
-    if t.dtype not in dtypes:
-        _refuse(where, f"{name} is {t.dtype}")
+def _addr(where: str, name: str, t: torch.Tensor, shape, dtype, dev: int) -> int:
+    """Address of a contiguous tensor on GPU `dev` of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        _refuse(where, f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
         _refuse(where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.device != dev:
-        _refuse(where, f"{name} is on {t.device}, not on {dev}")
-    if not t.is_contiguous():
-        _refuse(where, f"{name} is not contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        _refuse(where, f"{name} is on {t.device}, not on GPU {dev}")
+    _refuse(where, f"{name} is not contiguous")
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
-_F32 = (torch.float32,)
+def _lead(where: str, name: str, t: torch.Tensor):
+    """Shape, type and GPU of the tensor that the others have to match."""
+    dtype, shape = t.dtype, t.shape
+    if (dtype is not _f32 and dtype is not _bf16) or len(shape) != 2:
+        _refuse(where, f"{name} is {dtype} of shape {tuple(shape)}")
+    return shape, dtype, t.get_device()
 
 
-def _run(where: str, dev: torch.device, stream, call, args) -> None:
-    """One library call on `dev` and its current stream."""
-    if dev.type != "cuda":
-        _refuse(where, f"tensors are on {dev}")
-    if dev.index == torch.cuda.current_device():
-        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None
-                    else stream.cuda_stream), where)
-        return
-    with torch.cuda.device(dev):
-        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None
-                    else stream.cuda_stream), where)
+def _float(where: str, name: str, t: torch.Tensor):
+    dtype = t.dtype
+    if dtype is not _f32 and dtype is not _bf16:
+        _refuse(where, f"{name} is {dtype}")
+    return dtype
 
 
-def _finite(where: str, name: str, v) -> float:
-    v = float(v)
-    if not math.isfinite(v):
-        _refuse(where, f"{name} is {v}")
-    return v
+def _run(where: str, dev: int, stream, call, args) -> None:
+    """One library call on GPU `dev`, on its current stream unless one is given."""
+    if dev < 0:
+        _refuse(where, "tensors are on the cpu")
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                          else stream.cuda_stream)
+    else:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                      else stream.cuda_stream)
+    if status != BL_OK:
+        raise BitLinearError(status, where)
 
 
 def _one_of(where: str, name: str, v, table) -> int:
-    if isinstance(v, str):
-        if v not in table:
+    got = table.get(v)
+    if got is None:
+        if isinstance(v, str):
             _refuse(where, f"{name} is {v!r}, not one of {', '.join(table)}")
-        return table[v]
-    return int(v)
+        got = int(v)
+    return got
 
 
-def _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act, residual,
+def _check_scale(where: str, v) -> None:
+    if not -_FLT_MAX <= v <= _FLT_MAX:
+        _refuse(where, f"residual_scale is {v}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _segments(rows):
+    """Row counts as the C table (never written), their number and their sum."""
+    rows = (rows,) if isinstance(rows, int) else rows
+    return _seg_table(rows)
+
+
+_row_bytes = functools.lru_cache(maxsize=1024)(bitlinear_packed_row_bytes)
+
+
+def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act, residual,
                       residual_scale, out_dtype, y, z, stream):
     lay = _one_of(where, "layout", layout, LAYOUTS)
-    table, nseg, N = _seg_table((seg_rows,) if isinstance(seg_rows, int) else seg_rows)
+    table, nseg, N = _segments(seg_rows if isinstance(seg_rows, (int, tuple)) else tuple(seg_rows))
     if out_dtype is None:
-        out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.float32
-    if out_dtype not in _FLOATS:
+        out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else _f32
+    if out_dtype is not _f32 and out_dtype is not _bf16:
         _refuse(where, f"out_dtype is {out_dtype}")
+    shape = (M, N)
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+        y = torch.empty(shape, dtype=out_dtype, device=packed.device)
     want_z = z is not None and z is not False
     if z is True:
-        z = torch.empty((M, N), dtype=out_dtype, device=dev)
-    rb = bitlinear_packed_row_bytes(K, lay)
-    own = (out_dtype,)
-    if gammas.numel() < nseg or gammas.dtype != torch.float32 or gammas.device != dev:
-        _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for {nseg} segments")
-    if not gammas.is_contiguous():
-        _refuse(where, "gammas is not contiguous")
-    args = (_take(where, "packed", packed, (N, rb), (torch.uint8,), dev), lay, gammas.data_ptr(), table, nseg,
-            M, K, _take(where, "bias", bias, (N,), _FLOATS, dev),
+        z = torch.empty(shape, dtype=out_dtype, device=packed.device)
+    if (gammas.dtype is not _f32 or gammas.numel() < nseg or gammas.get_device() != dev
+            or not gammas.is_contiguous()):
+        _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for {nseg} segments, "
+                       "or is not contiguous")
+    _check_scale(where, residual_scale)
+    args = (*lead, _addr(where, "packed", packed, (N, _row_bytes(K, lay)), torch.uint8, dev), lay,
+            gammas.data_ptr(), table, nseg, M, K,
+            None if bias is None else _addr(where, "bias", bias, (N,), _float(where, "bias", bias), dev),
             BL_F32 if bias is None else _DTYPES[bias.dtype], _one_of(where, "act", act, ACTS),
-            _take(where, "residual", residual, (M, N), own, dev),
-            _finite(where, "residual_scale", residual_scale),
-            _take(where, "z", z, (M, N), own, dev) if want_z else None,
-            _take(where, "y", y, (M, N), own, dev), _DTYPES[out_dtype])
-    _run(where, dev, stream, getattr(_lib, where), lead + args)
+            None if residual is None else _addr(where, "residual", residual, shape, out_dtype, dev),
+            residual_scale, _addr(where, "z", z, shape, out_dtype, dev) if want_z else None,
+            _addr(where, "y", y, shape, out_dtype, dev), BL_F32 if out_dtype is _f32 else BL_BF16)
+    _run(where, dev, stream, call, args)
     return (y, z) if want_z else y
 
 
@@ -501,11 +526,10 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
     where = "bitlinear_forward_epilogue"
     if xq.dim() != 2:
         _refuse(where, f"xq has shape {tuple(xq.shape)}")
-    M, dev = xq.shape[0], xq.device
-    lead = (_take(where, "xq", xq, (M, K), (torch.int8,), dev),
-            _take(where, "scale", scale, (M,), _F32, dev))
-    return _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act,
-                             residual, residual_scale, out_dtype, y, z, stream)
+    M, dev = xq.shape[0], xq.get_device()
+    lead = (_addr(where, "xq", xq, (M, K), torch.int8, dev), _addr(where, "scale", scale, (M,), _f32, dev))
+    return _product_epilogue(where, _lib.bitlinear_forward_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
+                             layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
 
 
 def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
@@ -515,12 +539,11 @@ def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: tor
                               stream=None):
     """bitlinear_forward_epilogue fused with the quantisation of x, M <= 4 tokens."""
     where = "bitlinear_linear_epilogue"
-    if x.dim() != 2 or x.dtype not in _FLOATS:
-        _refuse(where, f"x is {x.dtype} of shape {tuple(x.shape)}")
-    (M, K), dev = x.shape, x.device
-    lead = (_take(where, "x", x, (M, K), _FLOATS, dev), _DTYPES[x.dtype])
-    return _product_epilogue(where, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act,
-                             residual, residual_scale, out_dtype, y, z, stream)
+    shape, dtype, dev = _lead(where, "x", x)
+    M, K = shape
+    lead = (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16)
+    return _product_epilogue(where, _lib.bitlinear_linear_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
+                             layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
 
 
 def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
@@ -529,22 +552,28 @@ def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor,
                     z: torch.Tensor | bool | None = None, stream=None):
     """``linear`` with bias, activation and residual: one fused launch for
     M <= 4, otherwise quantise then multiply."""
-    more = (layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
     if x.shape[0] <= FUSED_MAX_M:
-        return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, *more)
-    if x.device.index != torch.cuda.current_device():
-        with torch.cuda.device(x.device):
-            return linear_epilogue(x, packed, gammas, seg_rows, *more)
-    xq, scale = bitlinear_quant_acts(x, stream=stream)
-    return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, x.shape[1], *more)
+        return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
+                                         out_dtype, y, z, stream)
+    where = "linear_epilogue"
+    shape, dtype, dev = _lead(where, "x", x)
+    M, K = shape
+    xq = torch.empty(shape, dtype=torch.int8, device=x.device)
+    scale = torch.empty(M, dtype=_f32, device=x.device)
+    _run(where, dev, stream, _lib.bitlinear_quant_acts,
+         (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16, M, K, xq.data_ptr(),
+          scale.data_ptr()))
+    return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, K, layout, bias, act, residual,
+                                      residual_scale, out_dtype, y, z, stream)
 
 
-def _workspace(where: str, ws, need: int, dev):
+def _workspace(where: str, ws, need: int, t: torch.Tensor):
+    """Address and bytes of the caller's workspace, or of a new one beside t (held by the returned tensor)."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=t.device)
+    elif ws.get_device() != t.get_device() or not ws.is_contiguous():
         _refuse(where, "workspace is on another device or not contiguous")
-    return ws, ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 class EpilogueGrads(NamedTuple):
@@ -553,6 +582,7 @@ class EpilogueGrads(NamedTuple):
     grad_residual: torch.Tensor | None
 
 
+@functools.lru_cache(maxsize=1024)
 def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
     return int(_lib.bitlinear_epilogue_backward_workspace_bytes(M, N))
 
@@ -568,29 +598,35 @@ def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, ac
     grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
     None (leave out). z may be None for act "none"."""
     where = "bitlinear_epilogue_backward"
-    if grad_y.dim() != 2 or grad_y.dtype not in _FLOATS:
-        _refuse(where, f"grad_y is {grad_y.dtype} of shape {tuple(grad_y.shape)}")
-    (M, N), dev = grad_y.shape, grad_y.device
+    shape, dtype, dev = _lead(where, "grad_y", grad_y)
+    M, N = shape
+    own = grad_z is not None and grad_z is not True and grad_z is not False
     if out_dtype is None:
-        out_dtype = grad_z.dtype if isinstance(grad_z, torch.Tensor) else grad_y.dtype
-
-    def out(t, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=dev) if t is True else None if t is False else t
-
-    r = EpilogueGrads(out(grad_z, (M, N), out_dtype), out(grad_bias, (N,), torch.float32),
-                      out(grad_residual, (M, N), grad_y.dtype))
-    need = bitlinear_epilogue_backward_workspace_bytes(M, N) if r.grad_bias is not None else 0
-    ws, ws_bytes = _workspace(where, workspace, need, dev)
-    args = (_take(where, "grad_y", grad_y, (M, N), _FLOATS, dev), _DTYPES[grad_y.dtype],
-            _take(where, "z", z, (M, N), _FLOATS, dev), BL_F32 if z is None else _DTYPES[z.dtype],
-            _one_of(where, "act", act, ACTS), _finite(where, "residual_scale", residual_scale), M, N,
-            _take(where, "grad_z", r.grad_z, (M, N), (out_dtype,), dev),
-            _DTYPES[out_dtype] if out_dtype in _DTYPES else _refuse(where, f"out_dtype is {out_dtype}"),
-            _take(where, "grad_bias", r.grad_bias, (N,), _F32, dev),
-            _take(where, "grad_residual", r.grad_residual, (M, N), (grad_y.dtype,), dev),
-            ws.data_ptr(), ws_bytes)
+        out_dtype = grad_z.dtype if own else dtype
+    if out_dtype is not _f32 and out_dtype is not _bf16:
+        _refuse(where, f"out_dtype is {out_dtype}")
+    if not own:
+        grad_z = torch.empty(shape, dtype=out_dtype, device=grad_y.device) if grad_z else None
+    if grad_bias is True:
+        grad_bias = torch.empty(N, dtype=_f32, device=grad_y.device)
+    elif grad_bias is False:
+        grad_bias = None
+    if grad_residual is True:
+        grad_residual = torch.empty(shape, dtype=dtype, device=grad_y.device)
+    elif grad_residual is False:
+        grad_residual = None
+    _check_scale(where, residual_scale)
+    need = bitlinear_epilogue_backward_workspace_bytes(M, N) if grad_bias is not None else 0
+    hold, ws, ws_bytes = (None, None, 0) if need == 0 else _workspace(where, workspace, need, grad_y)
+    args = (_addr(where, "grad_y", grad_y, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16,
+            None if z is None else _addr(where, "z", z, shape, _float(where, "z", z), dev),
+            BL_F32 if z is None else _DTYPES[z.dtype], _one_of(where, "act", act, ACTS), residual_scale, M, N,
+            None if grad_z is None else _addr(where, "grad_z", grad_z, shape, out_dtype, dev), _DTYPES[out_dtype],
+            None if grad_bias is None else _addr(where, "grad_bias", grad_bias, (N,), _f32, dev),
+            None if grad_residual is None else _addr(where, "grad_residual", grad_residual, shape, dtype, dev),
+            ws, ws_bytes)
     _run(where, dev, stream, _lib.bitlinear_epilogue_backward, args)
-    return r
+    return EpilogueGrads(grad_z, grad_bias, grad_residual)
 
 
 class Norm(NamedTuple):
@@ -623,28 +659,28 @@ class BlockNormGrads(NamedTuple):
 _NO_NORM = Norm(BL_NORM_NONE)
 
 
-def _norm_args(where, M, K, dev, x_dtype, pre, post, gate):
-    """(post kind, weight, bias), (pre kind, weight, bias), p_dtype, (gate, gate_kind)."""
-    post, pre = post or _NO_NORM, pre or _NO_NORM
-    params = [t for t in (post.weight, post.bias, pre.weight, pre.bias) if t is not None]
-    kind = BL_GATE_NONE
-    if gate is not None:
-        kind = BL_GATE_TOKEN if gate.dim() == 2 else BL_GATE_CHANNEL
-        if kind == BL_GATE_CHANNEL:
-            params.append(gate)
-    p_dtype = params[0].dtype if params else torch.float32
-    if p_dtype not in _FLOATS:
-        _refuse(where, f"parameters are {p_dtype}")
-    own, row = (p_dtype,), (K,)
-
-    def side(name, s):
-        return (_one_of(where, f"{name}.kind", s.kind, NORMS),
-                _take(where, f"{name}.weight", s.weight, row, own, dev),
-                _take(where, f"{name}.bias", s.bias, row, own, dev))
-
-    g = _take(where, "gate", gate, (M, K) if kind == BL_GATE_TOKEN else row,
-              (x_dtype,) if kind == BL_GATE_TOKEN else own, dev)
-    return side("post", post), side("pre", pre), _DTYPES[p_dtype], (g, kind)
+def _norm_args(where, shape, dev, x_dtype, pre, post, gate):
+    """The parameters' arguments: (gate, gate kind, post kind, weight, bias, post
+    eps), (pre kind, weight, bias, pre eps), p_dtype."""
+    qk, qw, qb, qe = post or _NO_NORM
+    pk, pw, pb, pe = pre or _NO_NORM
+    row = shape[1:]
+    gk = BL_GATE_NONE if gate is None else BL_GATE_TOKEN if gate.dim() == 2 else BL_GATE_CHANNEL
+    first = qw if qw is not None else pw if pw is not None else qb if qb is not None else pb
+    if first is None and gk == BL_GATE_CHANNEL:
+        first = gate
+    P = _f32 if first is None else _float(where, "a parameter", first)
+    g = None
+    if gk:
+        g = _addr(where, "gate", gate, shape, x_dtype, dev) if gk == BL_GATE_TOKEN else \
+            _addr(where, "gate", gate, row, P, dev)
+    return ((g, gk, _one_of(where, "post.kind", qk, NORMS),
+             None if qw is None else _addr(where, "post.weight", qw, row, P, dev),
+             None if qb is None else _addr(where, "post.bias", qb, row, P, dev), qe),
+            (_one_of(where, "pre.kind", pk, NORMS),
+             None if pw is None else _addr(where, "pre.weight", pw, row, P, dev),
+             None if pb is None else _addr(where, "pre.bias", pb, row, P, dev), pe),
+            BL_F32 if P is _f32 else BL_BF16)
 
 
 def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
@@ -663,45 +699,45 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
     n, as bitlinear_quant_acts(n in fp32). stats (a buffer or True): what the
     backward call needs. h_out may be h."""
     where = "bitlinear_block_norm"
-    if h.dim() != 2 or h.dtype not in _FLOATS:
-        _refuse(where, f"h is {h.dtype} of shape {tuple(h.shape)}")
-    shape, dev = h.shape, h.device
+    shape, H, dev = _lead(where, "h", h)
     M, K = shape
-    x_dtype = block.dtype if block is not None else out_dtype or (n.dtype if n is not None else h.dtype)
-    if x_dtype not in _FLOATS or (out_dtype is not None and out_dtype != x_dtype):
-        _refuse(where, f"block is {x_dtype}, out_dtype {out_dtype}")
-    post_a, pre_a, p_dtype, (g, gate_kind) = _norm_args(where, M, K, dev, x_dtype, pre, post, gate)
+    if block is not None:
+        X = _float(where, "block", block)
+    else:
+        X = out_dtype or (n.dtype if n is not None else H)
+    if (X is not _f32 and X is not _bf16) or (out_dtype is not None and out_dtype is not X):
+        _refuse(where, f"block is {X}, out_dtype {out_dtype}")
+    post_a, pre_a, P = _norm_args(where, shape, dev, X, pre, post, gate)
     if block is not None and h_out is None:
-        h_out = torch.empty(shape, dtype=h.dtype, device=dev)
+        h_out = torch.empty(shape, dtype=H, device=h.device)
     if pre is None or not normed:
         if n is not None:
             _refuse(where, "n is given without a norm that writes it")
     elif n is None:
-        n = torch.empty(shape, dtype=x_dtype, device=dev)
-    quant = quant or xq is not None or scale is not None
-    if quant:
+        n = torch.empty(shape, dtype=X, device=h.device)
+    if quant or xq is not None or scale is not None:
         if xq is None:
-            xq = torch.empty(shape, dtype=torch.int8, device=dev)
+            xq = torch.empty(shape, dtype=torch.int8, device=h.device)
         if scale is None:
-            scale = torch.empty(max(M, 1), dtype=torch.float32, device=dev)[:M]
+            scale = torch.empty(M, dtype=_f32, device=h.device)
     if stats is True:
-        stats = torch.empty((M, 4), dtype=torch.float32, device=dev)
+        stats = torch.empty((M, 4), dtype=_f32, device=h.device)
     elif stats is False:
         stats = None
-    args = (_take(where, "h", h, shape, _FLOATS, dev), _DTYPES[h.dtype],
-            _take(where, "block", block, shape, _FLOATS, dev), _DTYPES[x_dtype],
-            _finite(where, "residual_scale", residual_scale), g, gate_kind,
-            *post_a, 1.0 if post is None else float(post.eps),
-            *pre_a, 1.0 if pre is None else float(pre.eps), p_dtype, M, K,
-            _take(where, "h_out", h_out, shape, (h.dtype,), dev),
-            _take(where, "n", n, shape, (x_dtype,), dev),
-            _take(where, "xq", xq, shape, (torch.int8,), dev),
-            _take(where, "scale", scale, (M,), _F32, dev),
-            _take(where, "stats", stats, (M, 4), _F32, dev))
+    _check_scale(where, residual_scale)
+    args = (_addr(where, "h", h, shape, H, dev), BL_F32 if H is _f32 else BL_BF16,
+            None if block is None else _addr(where, "block", block, shape, X, dev),
+            BL_F32 if X is _f32 else BL_BF16, residual_scale, *post_a, *pre_a, P, M, K,
+            None if h_out is None else _addr(where, "h_out", h_out, shape, H, dev),
+            None if n is None else _addr(where, "n", n, shape, X, dev),
+            None if xq is None else _addr(where, "xq", xq, shape, torch.int8, dev),
+            None if scale is None else _addr(where, "scale", scale, (M,), _f32, dev),
+            None if stats is None else _addr(where, "stats", stats, (M, 4), _f32, dev))
     _run(where, dev, stream, _lib.bitlinear_block_norm, args)
     return BlockNorm(h if block is None else h_out, n, xq, scale, stats)
 
 
+@functools.lru_cache(maxsize=1024)
 def bitlinear_block_norm_backward_workspace_bytes(M: int, K: int) -> int:
     return int(_lib.bitlinear_block_norm_backward_workspace_bytes(M, K))
 
@@ -724,48 +760,52 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
     them; grad_h_out: the gradient of h_out from its other uses (None: zero);
     grad_n: the gradient of n (None without pre), or of the quantised input
     (straight-through). Parameter gradients are fp32 [K] (a gate per token: [M, K]
-    of block's type); params=False leaves out those that no buffer is given for."""
+    of block's type); params=False leaves out those that no buffer is given for.
+    New [K] gradients of one call share one allocation."""
     where = "bitlinear_block_norm_backward"
-    if h_out.dim() != 2 or h_out.dtype not in _FLOATS:
-        _refuse(where, f"h_out is {h_out.dtype} of shape {tuple(h_out.shape)}")
-    shape, dev = h_out.shape, h_out.device
+    shape, H, dev = _lead(where, "h_out", h_out)
     M, K = shape
-    x_dtype = block.dtype if block is not None else h_out.dtype
-    if x_dtype not in _FLOATS:
-        _refuse(where, f"block is {x_dtype}")
-    post_a, pre_a, p_dtype, (g, gate_kind) = _norm_args(where, M, K, dev, x_dtype, pre, post, gate)
+    row = shape[1:]
+    X = H if block is None else _float(where, "block", block)
+    post_a, pre_a, P = _norm_args(where, shape, dev, X, pre, post, gate)
+    token = post_a[1] == BL_GATE_TOKEN
     if grad_h is None:
-        grad_h = torch.empty(shape, dtype=h_out.dtype, device=dev)
+        grad_h = torch.empty(shape, dtype=H, device=h_out.device)
     if grad_block is None and block is not None:
-        grad_block = torch.empty(shape, dtype=x_dtype, device=dev)
-
-    def sums(t, p):
-        return torch.empty(K, dtype=torch.float32, device=dev) if t is None and params and p is not None else t
-
-    if post is not None:
-        grad_post_weight, grad_post_bias = sums(grad_post_weight, post.weight), sums(grad_post_bias, post.bias)
-    if pre is not None:
-        grad_pre_weight, grad_pre_bias = sums(grad_pre_weight, pre.weight), sums(grad_pre_bias, pre.bias)
-    if gate_kind == BL_GATE_CHANNEL:
-        grad_gate = sums(grad_gate, gate)
-    elif gate_kind == BL_GATE_TOKEN and grad_gate is None and params:
-        grad_gate = torch.empty(shape, dtype=x_dtype, device=dev)
-    token = gate_kind == BL_GATE_TOKEN
-    ws, ws_bytes = _workspace(where, workspace, bitlinear_block_norm_backward_workspace_bytes(M, K), dev)
-    args = (_take(where, "grad_h_out", grad_h_out, shape, (h_out.dtype,), dev),
-            _take(where, "grad_n", grad_n, shape, _FLOATS, dev),
+        grad_block = torch.empty(shape, dtype=X, device=h_out.device)
+    if params:
+        # what has a parameter and no buffer: rows of one tensor, each at a 16-byte boundary
+        rows = torch.empty((5, (K + 3) & ~3), dtype=_f32, device=h_out.device)
+        rows = iter((rows if K % 4 == 0 else rows[:, :K]).unbind())
+        if post is not None:
+            if grad_post_weight is None and post.weight is not None:
+                grad_post_weight = next(rows)
+            if grad_post_bias is None and post.bias is not None:
+                grad_post_bias = next(rows)
+        if pre is not None:
+            if grad_pre_weight is None and pre.weight is not None:
+                grad_pre_weight = next(rows)
+            if grad_pre_bias is None and pre.bias is not None:
+                grad_pre_bias = next(rows)
+        if grad_gate is None and gate is not None:
+            grad_gate = torch.empty(shape, dtype=X, device=h_out.device) if token else next(rows)
+    _check_scale(where, residual_scale)
+    hold, ws, ws_bytes = _workspace(where, workspace, bitlinear_block_norm_backward_workspace_bytes(M, K), h_out)
+    args = (None if grad_h_out is None else _addr(where, "grad_h_out", grad_h_out, shape, H, dev),
+            None if grad_n is None else _addr(where, "grad_n", grad_n, shape, _float(where, "grad_n", grad_n), dev),
             BL_F32 if grad_n is None else _DTYPES[grad_n.dtype],
-            _take(where, "h_out", h_out, shape, _FLOATS, dev), _DTYPES[h_out.dtype],
-            _take(where, "block", block, shape, _FLOATS, dev), _DTYPES[x_dtype],
-            _take(where, "stats", stats, (M, 4), _F32, dev),
-            _finite(where, "residual_scale", residual_scale), g, gate_kind, *post_a, *pre_a[:2],
-            p_dtype, M, K, _take(where, "grad_h", grad_h, shape, (h_out.dtype,), dev),
-            _take(where, "grad_block", grad_block, shape, (x_dtype,), dev),
-            _take(where, "grad_gate", grad_gate, shape if token else (K,), (x_dtype,) if token else _F32, dev),
-            _take(where, "grad_post_weight", grad_post_weight, (K,), _F32, dev),
-            _take(where, "grad_post_bias", grad_post_bias, (K,), _F32, dev),
-            _take(where, "grad_pre_weight", grad_pre_weight, (K,), _F32, dev),
-            _take(where, "grad_pre_bias", grad_pre_bias, (K,), _F32, dev), ws.data_ptr(), ws_bytes)
+            _addr(where, "h_out", h_out, shape, H, dev), BL_F32 if H is _f32 else BL_BF16,
+            None if block is None else _addr(where, "block", block, shape, X, dev),
+            BL_F32 if X is _f32 else BL_BF16, _addr(where, "stats", stats, (M, 4), _f32, dev), residual_scale,
+            *post_a[:5], *pre_a[:2], P, M, K, _addr(where, "grad_h", grad_h, shape, H, dev),
+            None if grad_block is None else _addr(where, "grad_block", grad_block, shape, X, dev),
+            None if grad_gate is None else _addr(where, "grad_gate", grad_gate, shape if token else row,
+                                                 X if token else _f32, dev),
+            None if grad_post_weight is None else _addr(where, "grad_post_weight", grad_post_weight, row, _f32, dev),
+            None if grad_post_bias is None else _addr(where, "grad_post_bias", grad_post_bias, row, _f32, dev),
+            None if grad_pre_weight is None else _addr(where, "grad_pre_weight", grad_pre_weight, row, _f32, dev),
+            None if grad_pre_bias is None else _addr(where, "grad_pre_bias", grad_pre_bias, row, _f32, dev),
+            ws, ws_bytes)
     _run(where, dev, stream, _lib.bitlinear_block_norm_backward, args)
     return BlockNormGrads(grad_h, grad_block, grad_gate, grad_post_weight, grad_post_bias,
                           grad_pre_weight, grad_pre_bias)

@@ -76,6 +76,19 @@ __device__ __forceinline__ float group_sum(float v, float *red, int waves) {
     for (int w = 1; w < waves; ++w) s += red[w];
     return s;
 }
+// Two sums at once.
+__device__ __forceinline__ float2 group_sum2(float v, float w, float2 *red, int waves) {
+    float2 s = make_float2(wave_sum_dpp(v), wave_sum_dpp(w));
+    if (waves == 1) return s;
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
+    lds_barrier();
+    s = red[0];
+    for (int i = 1; i < waves; ++i) {
+        s.x += red[i].x;
+        s.y += red[i].y;
+    }
+    return s;
+}
 __device__ __forceinline__ float group_max0(float v, float *red, int waves) {
     v = wave_max0_dpp(v);
     if (waves == 1) return v;
@@ -384,6 +397,211 @@ __global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNo
 //   d = grad_h' + J_pre^T grad_n;  grad_h = res_scale d;  grad_block = J_post^T (gate d)
 // then the columns: sum_m of grad_n x^_pre, grad_n, (d g) x^_post and d g (g: a
 // gate per token, else 1); a gate per channel factors out of its sums.
+//
+// Rows that grad_holds_row() accepts take both in one kernel: a workgroup walks
+// a run of rows, each held in registers (one or two chunks of eight elements
+// per thread), with the next row's loads in flight while the current one is
+// reduced, and keeps its columns' sums in registers. The sums of a run (at most
+// kChunkRows rows) are fp32; block_norm_grad_sums_kernel adds the runs in fp64,
+// in a fixed order. @@BWD@@
+constexpr int64_t kChunkRows = 512;
+constexpr int kGradThreads = 512;  // at most: two waves of 256 registers per SIMD
+// One chunk per thread, or two for rows that vectors divide (single elements of
+// two chunks spill): longer rows go through the kernels below.
+inline bool grad_holds_row(int64_t K) { return K <= (K % 8 == 0 ? 2 : 1) * 8 * kGradThreads; }
+
+template <typename HT, typename XT, typename NT, typename PT, int J, bool BIAS, bool VEC>
+__global__ __launch_bounds__(kGradThreads) void block_norm_grad_kernel(const BlockNormGradArgs a,
+                                                                       int64_t runs, bool cols) {
+    using S = Share<J, VEC>;
+    __shared__ float2 red[2][2][kGradThreads / 64];  // [row parity][norm]
+    const int64_t K = a.K;
+    const int waves = blockDim.x / 64;
+    const S sh{(int)K, (int)threadIdx.x, (int)blockDim.x};
+    const float inv_k = 1.0f / (float)K;
+    const bool has_g = a.grad_h_out != nullptr, has_n = a.grad_n != nullptr;
+    const bool block = a.block != nullptr, token = a.gate_kind == kGateToken;
+    const bool post = a.post.kind != kNormNone;
+    const void *gc = a.gate_kind == kGateChannel ? a.gate : nullptr;
+    const int64_t m0 = a.M * blockIdx.x / runs, m1 = a.M * (blockIdx.x + 1) / runs;
+
+    // norm_pre's weight; norm_post's times a gate per channel. Kept with one
+    // chunk per thread; with two they would spill, and are read (from the L1) in
+    // each row.
+    float wn[8], wp[8];
+    if constexpr (J == 1) {
+        load_param<PT>(a.pre.weight, 0, sh, wn);
+        load_params<PT>(a.post.weight, gc, 0, sh, wp);
+    }
+    constexpr int kSums = BIAS ? 4 : 2;
+    float acc[kSums][J][8];
+#pragma unroll
+    for (int i = 0; i < kSums; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[i][j][e] = 0.f;
+
+    RowRegs<HT, J, VEC> rG, rh;
+    RowRegs<NT, J, VEC> rn;
+    RowRegs<XT, J, VEC> rb, rg;
+    float4 st_next;
+    auto load_row = [&](int64_t m) {
+        const int64_t at = m * K;
+        if (has_g) rG.load(static_cast<const HT *>(a.grad_h_out) + at, sh);
+        if (has_n) rn.load(static_cast<const NT *>(a.grad_n) + at, sh);
+        rh.load(static_cast<const HT *>(a.h_out) + at, sh);
+        if (block) rb.load(static_cast<const XT *>(a.block) + at, sh);
+        if (token) rg.load(static_cast<const XT *>(a.gate) + at, sh);
+        st_next = reinterpret_cast<const float4 *>(a.stats)[m];
+    };
+    if (m0 < m1) load_row(m0);
+    for (int64_t m = m0; m < m1; ++m) {
+        float d[J][8], g[J][8], hat[J][8], b[J][8], gt[J][8];
+        const float4 st = st_next;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[j][e] = g[j][e] = b[j][e] = 0.f, gt[j][e] = 1.f;
+            if (has_g) rG.widen(j, sh, d[j]);
+            if (has_n) rn.widen(j, sh, g[j]);
+            rh.widen(j, sh, hat[j]);
+            if (block) rb.widen(j, sh, b[j]);
+            if (token) rg.widen(j, sh, gt[j]);
+        }
+        if (m + 1 < m1) load_row(m + 1);
+        const int p = m & 1;
+
+        if (has_n) {
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if constexpr (J > 1) load_param<PT>(a.pre.weight, j, sh, wn);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    hat[j][e] = (hat[j][e] - st.z) * st.w;
+                    const float wv = g[j][e] * wn[e];
+                    acc[0][j][e] = __builtin_fmaf(g[j][e], hat[j][e], acc[0][j][e]);
+                    if constexpr (BIAS) acc[2][j][e] += g[j][e];
+                    g[j][e] = wv;
+                    s1 += wv;
+                    s2 = __builtin_fmaf(wv, hat[j][e], s2);
+                }
+            }
+            const float2 c = group_sum2(s1, s2, red[p][0], waves);
+            const float c1 = a.pre.kind == kNormLayer ? c.x * inv_k : 0.f, c2 = c.y * inv_k;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float t = st.w * (g[j][e] - c1 - hat[j][e] * c2);
+                    d[j][e] = sh.valid(j, e) ? d[j][e] + t : 0.f;
+                }
+        }
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float out[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[e] = block ? a.res_scale * d[j][e] : d[j][e];
+            store_share(static_cast<HT *>(a.grad_h) + m * K, j, sh, out);
+            if (!block) continue;
+            if constexpr (J > 1) load_params<PT>(a.post.weight, gc, j, sh, wp);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = d[j][e] * gt[j][e];
+                b[j][e] = (b[j][e] - st.x) * st.y;  // x^ of norm_post (b itself without it)
+                gt[j][e] = v * wp[e];
+                s1 += gt[j][e];
+                s2 = __builtin_fmaf(gt[j][e], b[j][e], s2);
+                acc[1][j][e] = __builtin_fmaf(v, b[j][e], acc[1][j][e]);
+                if constexpr (BIAS) acc[3][j][e] += v;
+            }
+            if (token && a.grad_gate) {
+                float pb[8];
+                if (a.post.bias) load_param<PT>(a.post.bias, j, sh, pb);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float pv = b[j][e] * wp[e];
+                    out[e] = d[j][e] * (a.post.bias ? pv + pb[e] : pv);
+                }
+                store_share(static_cast<XT *>(a.grad_gate) + m * K, j, sh, out);
+            }
+        }
+        if (!block) continue;
+        float e1 = 0.f, e2 = 0.f;
+        if (post) {
+            const float2 c = group_sum2(s1, s2, red[p][1], waves);
+            e1 = a.post.kind == kNormLayer ? c.x * inv_k : 0.f;
+            e2 = c.y * inv_k;
+        }
+        if (!a.grad_block) continue;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (post) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gt[j][e] = st.y * (gt[j][e] - e1 - b[j][e] * e2);
+            }
+            store_share(static_cast<XT *>(a.grad_block) + m * K, j, sh, gt[j]);
+        }
+    }
+    if (!cols) return;
+    float *part = a.workspace + (int64_t)blockIdx.x * kSums * K;
+#pragma unroll
+    for (int i = 0; i < kSums; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) store_share(part + i * K, j, sh, acc[i][j]);
+}
+
+// Sums of the runs' partials [runs][sums][K], in fp64: 32 columns of one sum per
+// workgroup, the runs split over its 32 rows of threads (of the 256 runs of a
+// full card each thread has eight loads, all in flight at once).
+constexpr int kSumRows = 32;
+// Order of the sums: grad_n x^_pre, (d g) x^_post, grad_n, d g.
+__device__ __forceinline__ double sum_runs(const float *part, int64_t stride, int64_t runs) {
+    __shared__ double red[kSumRows][33];
+    const int c = threadIdx.x % 32, r = threadIdx.x / 32;
+    double s = 0.0;
+    if (part) {
+#pragma unroll 8
+        for (int64_t i = r; i < runs; i += kSumRows) s += (double)part[i * stride];
+    }
+    __syncthreads();
+    red[r][c] = s;
+    __syncthreads();
+    s = red[0][c];
+#pragma unroll
+    for (int i = 1; i < kSumRows; ++i) s += red[i][c];
+    return s;
+}
+template <typename PT>
+__global__ __launch_bounds__(32 * kSumRows) void block_norm_grad_sums_kernel(const BlockNormGradArgs a,
+                                                                   const float *parts, int64_t runs,
+                                                                   int sums) {
+    const int64_t k = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+    const bool ok = k < a.K;
+    const int64_t stride = sums * a.K;
+    auto sum = [&](int i) { return sum_runs(ok && i < sums ? parts + i * a.K + k : nullptr, stride, runs); };
+    const bool write = ok && threadIdx.x < 32;
+    if (blockIdx.y == 0) {
+        const double s1 = sum(0), s0 = sums > 2 ? sum(2) : 0.0;
+        if (write && a.grad_pre_weight) a.grad_pre_weight[k] = (float)s1;
+        if (write && a.grad_pre_bias) a.grad_pre_bias[k] = (float)s0;
+        return;
+    }
+    const double s1 = sum(1), s0 = sums > 2 ? sum(3) : 0.0;
+    if (!write) return;
+    const bool gc = a.gate_kind == kGateChannel;
+    const double g = gc ? (double)param<PT>(a.gate, k, 1.f) : 1.0;
+    if (a.grad_post_weight) a.grad_post_weight[k] = (float)(g * s1);
+    if (a.grad_post_bias) a.grad_post_bias[k] = (float)(g * s0);
+    if (gc && a.grad_gate)
+        static_cast<float *>(a.grad_gate)[k] = (float)((double)param<PT>(a.post.weight, k, 1.f) * s1 +
+                                                       (double)param<PT>(a.post.bias, k, 0.f) * s0);
+}
+
+// Longer rows: a workgroup per row with a pass per statistic, then the columns
+// in a kernel of their own that forms d again.
 template <typename HT, typename XT, typename NT, typename PT>
 struct GradRow {
     const BlockNormGradArgs &a;
@@ -464,8 +682,7 @@ __global__ __launch_bounds__(kThreads) void block_norm_grad_rows_kernel(const Bl
 
 // Column sums over the rows of one chunk, in fp32: at most kChunkRows terms,
 // the chunks are then added in fp64 (block_norm_grad_sums_kernel).
-constexpr int kSums = 4;
-constexpr int64_t kChunkRows = 512;
+constexpr int kAllSums = 4;
 int64_t grad_chunks(int64_t M, int64_t K) {
     const int64_t col_blocks = (K + kThreads - 1) / kThreads;
     int64_t p = 2048 / col_blocks;  // about eight workgroups for each compute unit
@@ -480,46 +697,37 @@ __global__ __launch_bounds__(kThreads) void block_norm_grad_cols_kernel(const Bl
     const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (k >= a.K) return;
     const int64_t m0 = a.M * blockIdx.y / chunks, m1 = a.M * (blockIdx.y + 1) / chunks;
-    float s[kSums] = {0.f, 0.f, 0.f, 0.f};
+    float s[kAllSums] = {0.f, 0.f, 0.f, 0.f};
     for (int64_t m = m0; m < m1; ++m) {
         const GradRow<HT, XT, NT, PT> r(a, m);
         const float2 c = reinterpret_cast<const float2 *>(a.workspace)[m];
         if (r.gn) {
             const float g = r.grad_n(k);
             s[0] = __builtin_fmaf(g, r.pre_hat(k), s[0]);
-            s[1] += g;
+            s[2] += g;
         }
         if (r.b) {
             const float v = r.gated(r.d(k, c.x, c.y), k);
-            s[2] = __builtin_fmaf(v, r.post_hat(k), s[2]);
+            s[1] = __builtin_fmaf(v, r.post_hat(k), s[1]);
             s[3] += v;
         }
     }
-    float *out = a.workspace + 2 * a.M + (int64_t)blockIdx.y * kSums * a.K + k;
+    float *out = a.workspace + 2 * a.M + (int64_t)blockIdx.y * kAllSums * a.K + k;
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) out[i * a.K] = s[i];
+    for (int i = 0; i < kAllSums; ++i) out[i * a.K] = s[i];
 }
 
-template <typename PT>
-__global__ __launch_bounds__(kThreads) void block_norm_grad_sums_kernel(const BlockNormGradArgs a,
-                                                                        int64_t chunks) {
-    const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (k >= a.K) return;
-    double s[kSums] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t c = 0; c < chunks; ++c)
-#pragma unroll
-        for (int i = 0; i < kSums; ++i)
-            s[i] += (double)a.workspace[2 * a.M + (c * kSums + i) * a.K + k];
-    if (a.grad_pre_weight) a.grad_pre_weight[k] = (float)s[0];
-    if (a.grad_pre_bias) a.grad_pre_bias[k] = (float)s[1];
-    const bool gc = a.gate_kind == kGateChannel;
-    const double g = gc ? (double)param<PT>(a.gate, k, 1.f) : 1.0;
-    if (a.grad_post_weight) a.grad_post_weight[k] = (float)(g * s[2]);
-    if (a.grad_post_bias) a.grad_post_bias[k] = (float)(g * s[3]);
-    if (gc && a.grad_gate)
-        static_cast<float *>(a.grad_gate)[k] =
-            (float)((double)param<PT>(a.post.weight, k, 1.f) * s[2] +
-                    (double)param<PT>(a.post.bias, k, 0.f) * s[3]);
+// Threads of the fused kernel, and its runs of rows: as many workgroups as keep
+// kGradThreads threads on each of 256 compute units, at most kChunkRows rows each.
+int64_t grad_threads(int64_t K) {
+    const int64_t chunks = (K + 7) / 8;
+    return ((K <= 8 * kGradThreads ? chunks : (chunks + 1) / 2) + 63) / 64 * 64;
+}
+int64_t grad_runs(int64_t M, int64_t K) {
+    int64_t r = 256 * (kGradThreads / grad_threads(K));
+    if (r > M) r = M;
+    if (r < (M + kChunkRows - 1) / kChunkRows) r = (M + kChunkRows - 1) / kChunkRows;
+    return r;
 }
 
 // Calls go(float or uint16_t pointer) by a tensor's type.
@@ -564,15 +772,18 @@ hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
 }
 
 int64_t block_norm_grad_workspace(int64_t M, int64_t K) {
-    return 2 * M + grad_chunks(M, K) * kSums * K;
+    if (grad_holds_row(K)) return grad_runs(M, K) * kAllSums * K;
+    return 2 * M + grad_chunks(M, K) * kAllSums * K;
 }
 
 hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t stream) {
-    const int64_t chunks = grad_chunks(a.M, a.K);
-    const unsigned col_blocks = (unsigned)((a.K + kThreads - 1) / kThreads);
     const bool cols = a.grad_pre_weight || a.grad_pre_bias || a.grad_post_weight ||
                       a.grad_post_bias || (a.grad_gate && a.gate_kind == kGateChannel);
-    return typed(a.h_dtype, [&](auto h) {
+    // sums of grad_n and d g: for bias gradients, and for a channel gate's over a bias
+    const bool bias = a.grad_pre_bias || a.grad_post_bias ||
+                      (a.grad_gate && a.gate_kind == kGateChannel && a.post.bias);
+    const int64_t runs = grad_holds_row(a.K) ? grad_runs(a.M, a.K) : grad_chunks(a.M, a.K);
+    hipError_t e = typed(a.h_dtype, [&](auto h) {
         return typed(a.x_dtype, [&](auto x) {
             return typed(a.gn_dtype, [&](auto n) {
                 return typed(a.p_dtype, [&](auto p) {
@@ -580,23 +791,45 @@ hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t st
                     using XT = Pointee<decltype(x)>;
                     using NT = Pointee<decltype(n)>;
                     using PT = Pointee<decltype(p)>;
-                    if (a.M > 0) {
-                        hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>),
-                                           dim3((unsigned)a.M), dim3(kThreads), 0, stream, a);
-                        hipError_t e = hipGetLastError();
-                        if (e != hipSuccess || !cols) return e;
+                    if (grad_holds_row(a.K)) {
+                        auto go = [&](auto j_c, auto bias_c, auto vec_c) {
+                            hipLaunchKernelGGL(
+                                (block_norm_grad_kernel<HT, XT, NT, PT, decltype(j_c)::value,
+                                                        decltype(bias_c)::value, decltype(vec_c)::value>),
+                                dim3((unsigned)runs), dim3((unsigned)grad_threads(a.K)), 0, stream, a,
+                                runs, cols);
+                            return hipGetLastError();
+                        };
+                        auto biased = [&](auto j_c, auto vec_c) {
+                            return bias ? go(j_c, std::true_type{}, vec_c) : go(j_c, std::false_type{}, vec_c);
+                        };
+                        const std::integral_constant<int, 1> one;
+                        const std::integral_constant<int, 2> two;
+                        if (a.K <= 8 * kGradThreads)
+                            return a.K % 8 == 0 ? biased(one, std::true_type{}) : biased(one, std::false_type{});
+                        return biased(two, std::true_type{});
                     }
-                    hipLaunchKernelGGL((block_norm_grad_cols_kernel<HT, XT, NT, PT>),
-                                       dim3(col_blocks, (unsigned)chunks), dim3(kThreads), 0,
-                                       stream, a, chunks);
+                    hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>),
+                                       dim3((unsigned)a.M), dim3(kThreads), 0, stream, a);
                     hipError_t e = hipGetLastError();
-                    if (e != hipSuccess) return e;
-                    hipLaunchKernelGGL((block_norm_grad_sums_kernel<PT>), dim3(col_blocks),
-                                       dim3(kThreads), 0, stream, a, chunks);
+                    if (e != hipSuccess || !cols) return e;
+                    hipLaunchKernelGGL((block_norm_grad_cols_kernel<HT, XT, NT, PT>),
+                                       dim3((unsigned)((a.K + kThreads - 1) / kThreads), (unsigned)runs),
+                                       dim3(kThreads), 0, stream, a, runs);
                     return hipGetLastError();
                 });
             });
         });
+    });
+    if (e != hipSuccess || !cols) return e;
+    const bool fused = grad_holds_row(a.K);
+    const float *parts = a.workspace + (fused ? 0 : 2 * a.M);
+    const int sums = fused && !bias ? 2 : kAllSums;
+    const dim3 grid((unsigned)((a.K + 31) / 32), 2);
+    return typed(a.p_dtype, [&](auto p) {
+        hipLaunchKernelGGL((block_norm_grad_sums_kernel<Pointee<decltype(p)>>), grid,
+                           dim3(32 * kSumRows), 0, stream, a, parts, runs, sums);
+        return hipGetLastError();
     });
 }
 
