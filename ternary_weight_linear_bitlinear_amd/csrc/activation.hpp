@@ -89,28 +89,48 @@ __device__ __forceinline__ void activate_all(float (&z)[C], int act) {
     }
 }
 
-// act'(z); 0 at the corner of relu.
-__device__ __forceinline__ float activate_grad(float z, int act) {
+__device__ __forceinline__ float silu_slope(float z) {
+    const float p = sigmoid_fast(z);
+    return p * __builtin_fmaf(z, 1.0f - p, 1.0f);
+}
+__device__ __forceinline__ float gelu_erf_slope(float z) {
+    // Phi(z) + z phi(z)
+    const float g = half_gauss(z);
+    const float e = 0.5f * erfc_sqrt2(fabsf(z), g);
+    return __builtin_fmaf(z * kInvSqrt2Pi, g, z < 0.0f ? e : 1.0f - e);
+}
+__device__ __forceinline__ float gelu_tanh_slope(float z) {
+    const float zz = fminf(z * z, 1e4f);  // p is 0 or 1 long before; keeps 0 * du finite
+    const float p = sigmoid_fast(kGeluTanhC * z * __builtin_fmaf(kGeluTanhA, zz, 1.0f));
+    const float du = kGeluTanhC * __builtin_fmaf(3.0f * kGeluTanhA, zz, 1.0f);
+    return __builtin_fmaf(z * p * (1.0f - p), du, p);
+}
+
+// g = g * act'(z) for each element (relu's slope at 0 is 0).
+template <int C>
+__device__ __forceinline__ void times_slope(float (&g)[C], const float (&z)[C], int act) {
     switch (act) {
-        case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-        case kActRelu2: return 2.0f * fmaxf(z, 0.0f);
-        case kActSilu: {
-            const float p = sigmoid_fast(z);
-            return p * __builtin_fmaf(z, 1.0f - p, 1.0f);
-        }
-        case kActGelu: {
-            // Phi(z) + z phi(z)
-            const float g = half_gauss(z);
-            const float e = 0.5f * erfc_sqrt2(fabsf(z), g);
-            return __builtin_fmaf(z * kInvSqrt2Pi, g, z < 0.0f ? e : 1.0f - e);
-        }
-        case kActGeluTanh: {
-            const float zz = fminf(z * z, 1e4f);  // p is 0 or 1 long before; keeps 0 * du finite
-            const float p = sigmoid_fast(kGeluTanhC * z * __builtin_fmaf(kGeluTanhA, zz, 1.0f));
-            const float du = kGeluTanhC * __builtin_fmaf(3.0f * kGeluTanhA, zz, 1.0f);
-            return __builtin_fmaf(z * p * (1.0f - p), du, p);
-        }
-        default: return 1.0f;
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) g[e] = z[e] > 0.0f ? g[e] : 0.0f;
+            break;
+        case kActRelu2:
+#pragma unroll
+            for (int e = 0; e < C; ++e) g[e] = g[e] * (2.0f * fmaxf(z[e], 0.0f));
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) g[e] = g[e] * silu_slope(z[e]);
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) g[e] = g[e] * gelu_erf_slope(z[e]);
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int e = 0; e < C; ++e) g[e] = g[e] * gelu_tanh_slope(z[e]);
+            break;
+        default: break;
     }
 }
 
