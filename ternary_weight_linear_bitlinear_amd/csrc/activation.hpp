@@ -55,10 +55,14 @@ __device__ __forceinline__ float gelu_erf(float z) {
     const float x = fabsf(z);
     return __builtin_fmaf(-0.5f * x, erfc_sqrt2(x, half_gauss(z)), fmaxf(z, 0.0f));
 }
-__device__ __forceinline__ float gelu_tanh(float z) {
-    // z (1 + tanh(u)) / 2 = z sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3)
-    const float u2 = kGeluTanhC * z * __builtin_fmaf(kGeluTanhA * z, z, 1.0f);
-    return z * sigmoid_fast(u2);
+// sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3): 2^(-2 u log2 e) takes the constants in
+__device__ __forceinline__ float gelu_tanh_gate(float z, float zz) {
+    constexpr float k0 = -kLog2E * kGeluTanhC, k1 = k0 * kGeluTanhA;
+    const float e = __builtin_amdgcn_exp2f(z * __builtin_fmaf(k1, zz, k0));
+    return __builtin_amdgcn_rcpf(1.0f + e);
+}
+__device__ __forceinline__ float gelu_tanh(float z) {  // z (1 + tanh u) / 2 = z sigmoid(2 u)
+    return z * gelu_tanh_gate(z, z * z);
 }
 
 // z = act(z) for each element; one branch (uniform over a launch) for all C.
@@ -101,7 +105,7 @@ __device__ __forceinline__ float gelu_erf_slope(float z) {
 }
 __device__ __forceinline__ float gelu_tanh_slope(float z) {
     const float zz = fminf(z * z, 1e4f);  // p is 0 or 1 long before; keeps 0 * du finite
-    const float p = sigmoid_fast(kGeluTanhC * z * __builtin_fmaf(kGeluTanhA, zz, 1.0f));
+    const float p = gelu_tanh_gate(z, zz);
     const float du = kGeluTanhC * __builtin_fmaf(3.0f * kGeluTanhA, zz, 1.0f);
     return __builtin_fmaf(z * p * (1.0f - p), du, p);
 }

@@ -55,9 +55,15 @@ struct Epilogue {
                          : static_cast<const float *>(bias)[n];
     }
 
-    // bias of columns n .. n + C - 1 (0 past N, and without a bias)
+    // bias of columns n .. n + C - 1 (0 past N, and without a bias); n is a
+    // multiple of 4, the vector 16-byte aligned
     template <int C>
     __device__ __forceinline__ void load_bias(int64_t n, int64_t N, float (&b)[C]) const {
+        if (bias && n + C <= N) {
+            if (bias_bf16) Epilogue<uint16_t>::load(static_cast<const uint16_t *>(bias) + n, b);
+            else Epilogue<float>::load(static_cast<const float *>(bias) + n, b);
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < C; ++e) b[e] = bias && n + e < N ? bias_at(n + e) : 0.f;
     }
@@ -98,41 +104,50 @@ struct Epilogue {
         }
     }
 
-    // C consecutive outputs n .. n + C - 1 (those below N) of one token from
-    // their dequantised products v; `at` = the token's row offset + n in y, z
-    // and residual. vec: all C are below N and at * sizeof(YT) is aligned to
-    // C outputs.
+    // residual of C consecutive outputs (0 past N, and without one); `at` = the
+    // token's row offset + n in y, z and residual. vec: all C are below N and
+    // at * sizeof(YT) is aligned to C outputs.
     template <int C>
-    __device__ __forceinline__ void finish(float (&v)[C], const float (&b)[C], int64_t at, int64_t n,
-                                           int64_t N, bool vec, YT *y) const {
+    __device__ __forceinline__ void load_residual(int64_t at, int64_t n, int64_t N, bool vec,
+                                                  float (&r)[C]) const {
+        if (!residual) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) r[e] = 0.f;
+        } else if (vec) {
+            load(residual + at, r);
+        } else {
+#pragma unroll
+            for (int e = 0; e < C; ++e) r[e] = n + e < N ? widen(residual[at + e]) : 0.f;
+        }
+    }
+
+    // C consecutive outputs n .. n + C - 1 (those below N) of one token from
+    // their dequantised products v, bias b and residual r.
+    template <int C>
+    __device__ __forceinline__ void finish(float (&v)[C], const float (&b)[C], const float (&r)[C],
+                                           int64_t at, int64_t n, int64_t N, bool vec, YT *y) const {
         if (bias) {
 #pragma unroll
             for (int e = 0; e < C; ++e) v[e] += b[e];
         }
-        if (vec) {
-            float r[C];
-            if (residual) load(residual + at, r);
-            if (z) store(z + at, v);
-            activate_all(v, act);
-            if (residual) {
+        if (z) put(z, v, at, n, N, vec);
+        activate_all(v, act);
+        if (residual) {
 #pragma unroll
-                for (int e = 0; e < C; ++e) v[e] = __builtin_fmaf(res_scale, r[e], v[e]);
-            }
-            store(y + at, v);
+            for (int e = 0; e < C; ++e) v[e] = __builtin_fmaf(res_scale, r[e], v[e]);
+        }
+        put(y, v, at, n, N, vec);
+    }
+    template <int C>
+    __device__ __forceinline__ static void put(YT *p, const float (&v)[C], int64_t at, int64_t n,
+                                               int64_t N, bool vec) {
+        if (vec) {
+            store(p + at, v);
             return;
         }
-        if (z) {
 #pragma unroll
-            for (int e = 0; e < C; ++e)
-                if (n + e < N) z[at + e] = narrow(v[e]);
-        }
-        activate_all(v, act);
-#pragma unroll
-        for (int e = 0; e < C; ++e) {
-            if (n + e >= N) continue;
-            if (residual) v[e] = __builtin_fmaf(res_scale, widen(residual[at + e]), v[e]);
-            y[at + e] = narrow(v[e]);
-        }
+        for (int e = 0; e < C; ++e)
+            if (n + e < N) p[at + e] = narrow(v[e]);
     }
 #endif
 };

@@ -208,31 +208,41 @@ __device__ __forceinline__ void stage_fragment(int8_t *buf, const v16i &a, int c
         *reinterpret_cast<v4i *>(buf + frag_slot<BN>(frow, col / 4 + 2 * q + lg)) =
             v4i{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
 }
+// A row's factor, formed once (a full division): gamma * scale / 127 for one
+// matrix; scale / 127, for a column's gamma to multiply, in a stack. These are
+// the plain epilogue's products in its order.
+template <int BM, int T>
+__device__ __forceinline__ void stage_row_factors(float *rowf, const GammaMap &gm, float g0,
+                                                  const float *scale, int64_t m0, int64_t M) {
+    for (int r = threadIdx.x; r < BM; r += T) {
+        const float sm = scale[m0 + r < M ? m0 + r : M - 1];
+        rowf[r] = gm.nseg == 1 ? g0 * sm / 127.0f : sm / 127.0f;
+    }
+}
 // T threads; a thread keeps its eight columns (and their bias and gammas) over all rows.
 template <int BN, int T, typename YT, typename E>
 struct RowEpilogue {
     static constexpr int kPieces = BN / 8, kStep = T / kPieces;  // pieces a row, rows a step
     static_assert(T % kPieces == 0 && 32 % kStep == 0, "whole rows a step");
     const E &ep;
-    const float *scale;
+    const float *rowf;
     const bool one;
     const int64_t m0, n, M, N, ld;
     YT *y;
     bool vec;
     int row0, piece;
-    float g0, gam[8], bias[8];
+    float gam[8], bias[8];
     __device__ __forceinline__ RowEpilogue(const E &ep_, const GammaMap &gm,
-                                           const float (&gs)[kMaxSegments], const float *scale_,
+                                           const float (&gs)[kMaxSegments], const float *rowf_,
                                            int64_t m0_, int64_t n0, int64_t M_, int64_t N_,
                                            int64_t ld_, YT *y_)
-        : ep(ep_), scale(scale_), one(gm.nseg == 1), m0(m0_), n(n0 + (threadIdx.x % kPieces) * 8),
+        : ep(ep_), rowf(rowf_), one(gm.nseg == 1), m0(m0_), n(n0 + (threadIdx.x % kPieces) * 8),
           M(M_), N(N_), ld(ld_), y(y_) {
         row0 = threadIdx.x / kPieces;
         piece = threadIdx.x % kPieces;
         vec = n + 8 <= N && ld % (16 / (int)sizeof(YT)) == 0;
-        g0 = gs[0];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gam[e] = one ? g0 : seg_gamma(gm, gs, n + e);
+        for (int e = 0; e < 8; ++e) gam[e] = one ? 1.0f : seg_gamma(gm, gs, n + e);
         ep.load_bias(n, N, bias);
     }
     // 32 staged rows, tokens m0 + first ..
@@ -242,17 +252,20 @@ struct RowEpilogue {
         for (int r = row0; r < 32; r += kStep) {
             const int64_t m = m0 + first + r;
             if (m >= M) return;
+            float res[8];
+            ep.load_residual(m * ld + n, n, N, vec, res);
             const v4i lo = *reinterpret_cast<const v4i *>(buf + frag_slot<BN>(r, 2 * piece));
             const v4i hi = *reinterpret_cast<const v4i *>(buf + frag_slot<BN>(r, 2 * piece + 1));
-            const float sm = scale[m];
-            // the factors of the plain epilogue: gamma * scale / 127 for one
-            // matrix, gamma * (scale / 127) for a row of a stack
-            const float f1 = g0 * sm / 127.0f, s127 = sm / 127.0f;
+            const float f = rowf[first + r];
             float v[8];
+            if (one) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]) * (one ? f1 : gam[e] * s127);
-            ep.finish(v, bias, m * ld + n, n, N, vec, y);
+                for (int e = 0; e < 8; ++e) v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]) * f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]) * (gam[e] * f);
+            }
+            ep.finish(v, bias, res, m * ld + n, n, N, vec, y);
         }
     }
 };
@@ -603,7 +616,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     if constexpr (E::kActive) {
         static_assert(WM == 1, "a fragment row is staged by one row of waves");
         constexpr int FP = C::template kEpiFrags<E>;  // fragment rows staged at a time
-        const RowEpilogue<BN, kThreads, YT, E> rows(ep, gm, gs, scale, m0, n0, M, N, ldy, y);
+        __shared__ float rowf[BM];
+        stage_row_factors<BM, kThreads>(rowf, gm, gs[0], scale, m0, M);
+        const RowEpilogue<BN, kThreads, YT, E> rows(ep, gm, gs, rowf, m0, n0, M, N, ldy, y);
         if constexpr (KG > 1) lds_barrier();  // the other groups' sums have been read
 #pragma unroll
         for (int i0 = 0; i0 < C::FI; i0 += FP) {
@@ -920,7 +935,9 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
         lds_barrier();
         float gse[kMaxSegments];
         load_gammas(gm, gse);
-        const RowEpilogue<256, 512, YT, E> rows(ep, gm, gse, scale, m0, n0, M, g.N, ldy, y);
+        __shared__ float rowf[BM];
+        stage_row_factors<BM, 512>(rowf, gm, gse[0], scale, m0, M);
+        const RowEpilogue<256, 512, YT, E> rows(ep, gm, gse, rowf, m0, n0, M, g.N, ldy, y);
         int8_t *const bufs[4] = {dma_s0, dma_s1, dma_s2, reinterpret_cast<int8_t *>(dma_out)};
         static_assert(kDmaStage == 32 * 256 * 4 && 64 * kDmaOutRow >= kDmaStage, "a fragment row fits");
 #pragma unroll
