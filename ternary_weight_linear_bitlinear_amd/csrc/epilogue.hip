@@ -69,8 +69,10 @@ __global__ __launch_bounds__(kThreads) void epilogue_grad_kernel(const EpilogueG
         }
     }
     if (!a.grad_bias) return;
+    const int start = sh.start(0), skip = sh.skip(0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[r][sh.index(0, e)] = s[e];
+    for (int e = 0; e < 8; ++e)
+        if (e >= skip) red[r][start + e] = s[e];
     __syncthreads();
     if ((int)threadIdx.x >= left) return;
     float t = red[0][threadIdx.x];
@@ -78,6 +80,29 @@ __global__ __launch_bounds__(kThreads) void epilogue_grad_kernel(const EpilogueG
     for (int i = 1; i < kRows; ++i) t += red[i][threadIdx.x];
     float *out = runs == 1 ? a.grad_bias : a.workspace + blockIdx.y * a.N;
     out[n0 + threadIdx.x] = t;
+}
+
+// Fewer than eight columns: a thread for each, over a run of rows.
+template <typename GT, typename ZT, typename OT>
+__global__ __launch_bounds__(64) void epilogue_grad_few_kernel(const EpilogueGradArgs a,
+                                                               int64_t runs) {
+    const int64_t n = threadIdx.x;
+    if (n >= a.N) return;
+    const int64_t m0 = a.M * blockIdx.x / runs, m1 = a.M * (blockIdx.x + 1) / runs;
+    float s = 0.f;
+    for (int64_t m = m0; m < m1; ++m) {
+        const int64_t at = m * a.N + n;
+        const float y = Elem<GT>::get(static_cast<const GT *>(a.grad_y), at);
+        if (a.grad_residual) put(static_cast<GT *>(a.grad_residual), at, a.res_scale * y);
+        float g[1] = {y};
+        if (a.act != kActNone) {
+            const float z[1] = {Elem<ZT>::get(static_cast<const ZT *>(a.z), at)};
+            times_slope(g, z, a.act);
+        }
+        if (a.grad_z) put(static_cast<OT *>(a.grad_z), at, g[0]);
+        s += g[0];
+    }
+    if (a.grad_bias) (runs == 1 ? a.grad_bias : a.workspace + blockIdx.x * a.N)[n] = s;
 }
 
 // grad_bias from the runs' partials, in fp64: 32 columns per workgroup, the runs
@@ -131,7 +156,14 @@ hipError_t launch_epilogue_backward(const EpilogueGradArgs &a, hipStream_t strea
                     return runs == 1 ? go(std::integral_constant<int, kNarrow>{}, vec_c)
                                      : go(std::integral_constant<int, kWide>{}, vec_c);
                 };
-                hipError_t e = a.N % 8 == 0 ? pieces(std::true_type{}) : pieces(std::false_type{});
+                hipError_t e;
+                if (a.N < 8) {
+                    hipLaunchKernelGGL((epilogue_grad_few_kernel<GT, ZT, OT>), dim3((unsigned)runs),
+                                       dim3(64), 0, stream, a, runs);
+                    e = hipGetLastError();
+                } else {
+                    e = a.N % 8 == 0 ? pieces(std::true_type{}) : pieces(std::false_type{});
+                }
                 if (e != hipSuccess || !a.grad_bias || runs == 1) return e;
                 hipLaunchKernelGGL(epilogue_grad_sums_kernel, dim3((unsigned)((a.N + 31) / 32)),
                                    dim3(kThreads), 0, stream, a.workspace, a.grad_bias, a.N, runs);

@@ -47,52 +47,64 @@ __device__ __forceinline__ float block_max(float v) {
 // Forward, rows that holds_row() accepts: one workgroup per row, the row held in registers
 // from its one read to its one write. Memory-bound; @@FWD@@
 //
-// Thread t owns J chunks of eight consecutive elements (chunks t, t + T, ...),
-// or, where K % 8 leaves rows unaligned, 8 J single elements T apart (VEC =
-// false). Every load of the row is issued before the first reduction. A
+// Thread t owns J chunks of eight consecutive elements (chunks t, t + T, ...;
+// row_share.hpp). Every load of the row is issued before the first reduction. A
 // statistic is a sum in fp32 over at most 8 J elements of a thread, a wave's 64
-// lanes and 16 waves, so at most 8 J + 22 additions follow one another.
+// lanes and 16 waves, so at most 8 J + 10 additions follow one another.
 constexpr int kMaxWaves = 16;
 constexpr int64_t kRegElems = 8 * 64 * kMaxWaves;  // of a row, for each chunk per thread
-// Four chunks fit the registers in vector form only (single elements spill), so
-// unaligned rows past two go through the row's passes instead.
-inline bool holds_row(int64_t K) { return K <= (K % 8 == 0 ? 4 : 2) * kRegElems; }
+inline bool holds_row(int64_t K) { return K >= 8 && K <= 4 * kRegElems; }
 
-// Sum (or maximum of values >= 0) over the workgroup; `red` is this reduction's
-// own, so one barrier is enough.
+// Reductions over the workgroup. Each wave leaves its value in `red`, which is
+// this reduction's own, so one barrier is enough; then every thread reads all of
+// them, four to a load and all loads at once (one by one, the LDS latency
+// of up to 16 waves' values cost more than the rest of the reduction). Entries of
+// absent waves are zero (clear_absent(), before the first barrier).
+__device__ __forceinline__ void clear_absent(float *red, int slots, int waves) {
+    for (int i = threadIdx.x; i < slots * kMaxWaves; i += blockDim.x)
+        if (i % kMaxWaves >= waves) red[i] = 0.f;
+}
+template <typename OP>
+__device__ __forceinline__ float across_waves(const float *red, int waves, OP op) {
+    const float4 *q = reinterpret_cast<const float4 *>(red);
+    auto of = [&](const float4 &a) { return op(op(a.x, a.y), op(a.z, a.w)); };
+    if (waves <= 4) return of(q[0]);
+    if (waves <= 8) {
+        const float4 a = q[0], b = q[1];
+        return op(of(a), of(b));
+    }
+    const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+    return op(op(of(a), of(b)), op(of(c), of(d)));
+}
 __device__ __forceinline__ float group_sum(float v, float *red, int waves) {
     v = wave_sum_dpp(v);
     if (waves == 1) return v;
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
     lds_barrier();
-    float s = red[0];
-    for (int w = 1; w < waves; ++w) s += red[w];
-    return s;
+    return across_waves(red, waves, [](float a, float b) { return a + b; });
 }
-// Two sums at once.
-__device__ __forceinline__ float2 group_sum2(float v, float w, float2 *red, int waves) {
-    float2 s = make_float2(wave_sum_dpp(v), wave_sum_dpp(w));
-    if (waves == 1) return s;
-    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
-    lds_barrier();
-    s = red[0];
-    for (int i = 1; i < waves; ++i) {
-        s.x += red[i].x;
-        s.y += red[i].y;
+// Two sums at once; red: 2 kMaxWaves entries.
+__device__ __forceinline__ float2 group_sum2(float v, float w, float *red, int waves) {
+    v = wave_sum_dpp(v);
+    w = wave_sum_dpp(w);
+    if (waves == 1) return make_float2(v, w);
+    if (threadIdx.x % 64 == 0) {
+        red[threadIdx.x / 64] = v;
+        red[kMaxWaves + threadIdx.x / 64] = w;
     }
-    return s;
+    lds_barrier();
+    auto add = [](float a, float b) { return a + b; };
+    return make_float2(across_waves(red, waves, add), across_waves(red + kMaxWaves, waves, add));
 }
-__device__ __forceinline__ float group_max0(float v, float *red, int waves) {
+__device__ __forceinline__ float group_max0(float v, float *red, int waves) {  // of values >= 0
     v = wave_max0_dpp(v);
     if (waves == 1) return v;
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
     lds_barrier();
-    float s = red[0];
-    for (int w = 1; w < waves; ++w) s = fmaxf(s, red[w]);
-    return s;
+    return across_waves(red, waves, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Chunk j of a [K] parameter vector in fp32: zero past K, ones without the vector.
+// Chunk j of a [K] parameter vector in fp32, ones without the vector.
 template <typename PT, int J, bool VEC>
 __device__ __forceinline__ void load_param(const void *p, int j, const Share<J, VEC> &sh, float (&w)[8]) {
     if (!p) {
@@ -100,15 +112,9 @@ __device__ __forceinline__ void load_param(const void *p, int j, const Share<J, 
         for (int e = 0; e < 8; ++e) w[e] = 1.0f;
         return;
     }
-    const PT *q = static_cast<const PT *>(p);
-    if constexpr (VEC) {
-        Raw8<PT> r;
-        r.load(q + (sh.valid(j, 0) ? sh.index(j, 0) : 0));
-        r.widen(w);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = Elem<PT>::get(q, sh.valid(j, e) ? sh.index(j, e) : 0);
-    }
+    Raw8<PT> r;
+    load_chunk(static_cast<const PT *>(p), j, sh, r);
+    r.widen(w);
 }
 // The same times a second vector.
 template <typename PT, int J, bool VEC>
@@ -124,9 +130,10 @@ __device__ __forceinline__ void load_params(const void *p, const void *q, int j,
 
 template <typename HT, typename XT, typename PT, int J, bool VEC>
 __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockNormArgs a) {
-    __shared__ float red[5][kMaxWaves];
+    __shared__ __attribute__((aligned(16))) float red[5][kMaxWaves];
     const int64_t m = blockIdx.x, K = a.K;
     const int waves = blockDim.x / 64;
+    clear_absent(red[0], 5, waves);
     const Share<J, VEC> sh{(int)K, (int)threadIdx.x, (int)blockDim.x};
     const float inv_k = 1.0f / (float)K;
     const bool block = a.block != nullptr, token = a.gate_kind == kGateToken;
@@ -141,10 +148,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
     // chunk per thread the parameters are fetched along with the row; with more
     // they would spill, and come (from L2) where they are used.
     constexpr bool kEarly = J == 1;
-    float wp[8], wn[8];
+    float wp[8], wn[8], pb[8], nb[8];
     if constexpr (kEarly) {
         load_params<PT>(a.post.weight, gc, 0, sh, wp);
         load_param<PT>(a.pre.weight, 0, sh, wn);
+        if (a.post.bias) load_params<PT>(a.post.bias, gc, 0, sh, pb);
+        if (a.pre.bias) load_param<PT>(a.pre.bias, 0, sh, nb);
     }
 
     // mean and 1 / deviation of the share x (zero past K)
@@ -163,12 +172,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
             t = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+            float d[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = sh.valid(j, e) ? x[j][e] - mean : 0.f;
-                t = __builtin_fmaf(d, d, t);
-            }
+            for (int e = 0; e < 8; ++e) d[e] = x[j][e] - mean;
+            if (s.kind == kNormLayer) clear_past(j, sh, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t = __builtin_fmaf(d[e], d[e], t);
+        }
         rstd = 1.0f / sqrtf(group_sum(t, red1, waves) * inv_k + s.eps);
     };
 
@@ -187,8 +198,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[j][e] = (b[j][e] - mean_b) * wp[e] * rstd_b;
             if (a.post.bias) {
-                float pb[8];
-                load_params<PT>(a.post.bias, gc, j, sh, pb);
+                if constexpr (!kEarly) load_params<PT>(a.post.bias, gc, j, sh, pb);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) b[j][e] += pb[e];
             }
@@ -203,8 +213,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 #pragma unroll
         for (int j = 0; j < J; ++j) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[j][e] = sh.valid(j, e) ? __builtin_fmaf(a.res_scale, v[j][e], b[j][e]) : 0.f;
+            for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf(a.res_scale, v[j][e], b[j][e]);
+            clear_past(j, sh, v[j]);
             store_share(out, j, sh, v[j]);
         }
     }
@@ -218,10 +228,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = (v[j][e] - mean_h) * wn[e] * rstd_h;
         if (a.pre.bias) {
-            float pb[8];
-            load_param<PT>(a.pre.bias, j, sh, pb);
+            if constexpr (!kEarly) load_param<PT>(a.pre.bias, j, sh, nb);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] += pb[e];
+            for (int e = 0; e < 8; ++e) v[j][e] += nb[e];
         }
     }
     if (a.n) {
@@ -232,30 +241,34 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
     if (a.xq) {
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+            clear_past(j, sh, v[j]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, sh.valid(j, e) ? fabsf(v[j][e]) : 0.f);
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[j][e]));
+        }
         const float s = fmaxf(group_max0(top, red[4], waves), 1e-6f);
         const float y = 1.0f / s;
         if (threadIdx.x == 0) a.scale[m] = s;
         int8_t *out = a.xq + m * K;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            if constexpr (VEC) {
-                if (sh.valid(j, 0))
-                    *reinterpret_cast<uint2 *>(out + sh.index(j, 0)) =
-                        make_uint2(quant4(v[j][0], v[j][1], v[j][2], v[j][3], s, y),
-                                   quant4(v[j][4], v[j][5], v[j][6], v[j][7], s, y));
-            } else {
+            int8_t *p = out + sh.start(j);
+            const int skip = sh.skip(j);
+            if (skip == 0) {
+                const uint32_t lo = quant4(v[j][0], v[j][1], v[j][2], v[j][3], s, y);
+                const uint32_t hi = quant4(v[j][4], v[j][5], v[j][6], v[j][7], s, y);
+                if constexpr (VEC) *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+                else *reinterpret_cast<Bytes8 *>(p) = Bytes8{{lo, hi}};
+            } else if constexpr (!VEC) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (sh.valid(j, e)) out[sh.index(j, e)] = quant1(v[j][e], s, y);
+                for (int e = 1; e < 8; ++e)
+                    if (e >= skip) p[e] = quant1(v[j][e], s, y);
             }
         }
     }
 }
 
-// Longer rows: one row per workgroup, any K: each statistic is a pass over the row (which
+// Other rows: one row per workgroup, any K: each statistic is a pass over the row (which
 // stays in the caches), the last pass writes. Every element is read and written
 // by one thread, and nothing is written before the last pass, so h_out may be h.
 template <typename HT, typename XT, typename PT>
@@ -337,17 +350,16 @@ __global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNo
 // in a fixed order. @@BWD@@
 constexpr int64_t kChunkRows = 512;
 constexpr int kGradThreads = 512;  // at most: two waves of 256 registers per SIMD
-// One chunk per thread, or two for rows that vectors divide (single elements of
-// two chunks spill): longer rows go through the kernels below.
-inline bool grad_holds_row(int64_t K) { return K <= (K % 8 == 0 ? 2 : 1) * 8 * kGradThreads; }
+inline bool grad_holds_row(int64_t K) { return K >= 8 && K <= 2 * 8 * kGradThreads; }
 
 template <typename HT, typename XT, typename NT, typename PT, int J, bool BIAS, bool VEC>
 __global__ __launch_bounds__(kGradThreads) void block_norm_grad_kernel(const BlockNormGradArgs a,
                                                                        int64_t runs, bool cols) {
     using S = Share<J, VEC>;
-    __shared__ float2 red[2][2][kGradThreads / 64];  // [row parity][norm]
+    __shared__ __attribute__((aligned(16))) float red[2][2][2 * kMaxWaves];  // [row parity][norm]
     const int64_t K = a.K;
     const int waves = blockDim.x / 64;
+    clear_absent(red[0][0], 8, waves);
     const S sh{(int)K, (int)threadIdx.x, (int)blockDim.x};
     const float inv_k = 1.0f / (float)K;
     const bool has_g = a.grad_h_out != nullptr, has_n = a.grad_n != nullptr;
@@ -422,12 +434,11 @@ __global__ __launch_bounds__(kGradThreads) void block_norm_grad_kernel(const Blo
             const float2 c = group_sum2(s1, s2, red[p][0], waves);
             const float c1 = a.pre.kind == kNormLayer ? c.x * inv_k : 0.f, c2 = c.y * inv_k;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float t = st.w * (g[j][e] - c1 - hat[j][e] * c2);
-                    d[j][e] = sh.valid(j, e) ? d[j][e] + t : 0.f;
-                }
+                for (int e = 0; e < 8; ++e) d[j][e] += st.w * (g[j][e] - c1 - hat[j][e] * c2);
+                clear_past(j, sh, d[j]);
+            }
         }
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -489,39 +500,43 @@ __global__ __launch_bounds__(kGradThreads) void block_norm_grad_kernel(const Blo
 // full card each thread has eight loads, all in flight at once).
 constexpr int kSumRows = 32;
 // Order of the sums: grad_n x^_pre, (d g) x^_post, grad_n, d g.
-__device__ __forceinline__ double sum_runs(const float *part, int64_t stride, int64_t runs) {
-    __shared__ double red[kSumRows][33];
-    const int c = threadIdx.x % 32, r = threadIdx.x / 32;
-    double s = 0.0;
-    if (part) {
+template <typename PT>
+__global__ __launch_bounds__(32 * kSumRows) void block_norm_grad_sums_kernel(
+    const BlockNormGradArgs a, const float *parts, int64_t runs, int sums) {
+    __shared__ double red[2][kSumRows][33];
+    const int c = threadIdx.x % 32, r = threadIdx.x / 32, y = blockIdx.y;
+    const int64_t k = (int64_t)blockIdx.x * 32 + c, stride = sums * a.K;
+    const bool biased = sums > 2;
+    double s1 = 0.0, s0 = 0.0;  // of norm_pre (y = 0) or norm_post (y = 1)
+    if (k < a.K) {
+        const float *p1 = parts + y * a.K + k, *p0 = p1 + 2 * a.K;
 #pragma unroll 8
-        for (int64_t i = r; i < runs; i += kSumRows) s += (double)part[i * stride];
+        for (int64_t i = r; i < runs; i += kSumRows) {
+            s1 += (double)p1[i * stride];
+            if (biased) s0 += (double)p0[i * stride];
+        }
+    }
+    red[0][r][c] = s1;
+    red[1][r][c] = s0;
+    __syncthreads();
+    // two rows of threads finish: 0 the first sum, 1 the second
+    if (r < 2) {
+        double s = 0.0;
+        if (r == 0 || biased) {
+#pragma unroll
+            for (int i = 0; i < kSumRows; ++i) s += red[r][i][c];
+        }
+        red[r][0][c] = s;
     }
     __syncthreads();
-    red[r][c] = s;
-    __syncthreads();
-    s = red[0][c];
-#pragma unroll
-    for (int i = 1; i < kSumRows; ++i) s += red[i][c];
-    return s;
-}
-template <typename PT>
-__global__ __launch_bounds__(32 * kSumRows) void block_norm_grad_sums_kernel(const BlockNormGradArgs a,
-                                                                   const float *parts, int64_t runs,
-                                                                   int sums) {
-    const int64_t k = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
-    const bool ok = k < a.K;
-    const int64_t stride = sums * a.K;
-    auto sum = [&](int i) { return sum_runs(ok && i < sums ? parts + i * a.K + k : nullptr, stride, runs); };
-    const bool write = ok && threadIdx.x < 32;
-    if (blockIdx.y == 0) {
-        const double s1 = sum(0), s0 = sums > 2 ? sum(2) : 0.0;
-        if (write && a.grad_pre_weight) a.grad_pre_weight[k] = (float)s1;
-        if (write && a.grad_pre_bias) a.grad_pre_bias[k] = (float)s0;
+    if (r > 0 || k >= a.K) return;
+    s1 = red[0][0][c];
+    s0 = red[1][0][c];
+    if (y == 0) {
+        if (a.grad_pre_weight) a.grad_pre_weight[k] = (float)s1;
+        if (a.grad_pre_bias) a.grad_pre_bias[k] = (float)s0;
         return;
     }
-    const double s1 = sum(1), s0 = sums > 2 ? sum(3) : 0.0;
-    if (!write) return;
     const bool gc = a.gate_kind == kGateChannel;
     const double g = gc ? (double)param<PT>(a.gate, k, 1.f) : 1.0;
     if (a.grad_post_weight) a.grad_post_weight[k] = (float)(g * s1);
@@ -531,7 +546,7 @@ __global__ __launch_bounds__(32 * kSumRows) void block_norm_grad_sums_kernel(con
                                                        (double)param<PT>(a.post.bias, k, 0.f) * s0);
 }
 
-// Longer rows: a workgroup per row with a pass per statistic, then the columns
+// Other rows: a workgroup per row with a pass per statistic, then the columns
 // in a kernel of their own that forms d again.
 template <typename HT, typename XT, typename NT, typename PT>
 struct GradRow {
@@ -685,9 +700,8 @@ hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
                 };
                 auto chunks = [&](auto vec_c) {
                     if (a.K <= kRegElems) return go(std::integral_constant<int, 1>{}, vec_c);
-                    if constexpr (decltype(vec_c)::value)
-                        if (a.K > 2 * kRegElems) return go(std::integral_constant<int, 4>{}, vec_c);
-                    return go(std::integral_constant<int, 2>{}, vec_c);
+                    if (a.K <= 2 * kRegElems) return go(std::integral_constant<int, 2>{}, vec_c);
+                    return go(std::integral_constant<int, 4>{}, vec_c);
                 };
                 return a.K % 8 == 0 ? chunks(std::true_type{}) : chunks(std::false_type{});
             });
@@ -729,9 +743,10 @@ hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t st
                         };
                         const std::integral_constant<int, 1> one;
                         const std::integral_constant<int, 2> two;
-                        if (a.K <= 8 * kGradThreads)
-                            return a.K % 8 == 0 ? biased(one, std::true_type{}) : biased(one, std::false_type{});
-                        return biased(two, std::true_type{});
+                        auto chunks = [&](auto vec_c) {
+                            return a.K <= 8 * kGradThreads ? biased(one, vec_c) : biased(two, vec_c);
+                        };
+                        return a.K % 8 == 0 ? chunks(std::true_type{}) : chunks(std::false_type{});
                     }
                     hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>),
                                        dim3((unsigned)a.M), dim3(kThreads), 0, stream, a);
