@@ -90,6 +90,30 @@ __device__ __forceinline__ float group_sum(float v, float *red, int waves) {
     lds_barrier();
     return across_waves(red, waves, [](float a, float b) { return a + b; });
 }
+// The same of one value for each of a thread's J chunks, added in the order in which
+// workgroups of J times the threads would add one each, so that a row's result
+// does not depend on how many rows go with it. (Rows of more chunks than 16 waves hold
+// always take the same J, and their threads add their own first.)
+template <int J>
+__device__ __forceinline__ float group_sum_chunks(const float (&v)[J], float *red, int waves) {
+    if constexpr (J == 1) {
+        return group_sum(v[0], red, waves);
+    } else {
+        if (J * waves > kMaxWaves) {
+            float t = v[0];
+#pragma unroll
+            for (int j = 1; j < J; ++j) t += v[j];
+            return group_sum(t, red, waves);
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float t = wave_sum_dpp(v[j]);
+            if (threadIdx.x % 64 == 0) red[j * waves + threadIdx.x / 64] = t;
+        }
+        lds_barrier();
+        return across_waves(red, J * waves, [](float a, float b) { return a + b; });
+    }
+}
 // Two sums at once; red: 2 kMaxWaves entries.
 __device__ __forceinline__ float2 group_sum2(float v, float w, float *red, int waves) {
     v = wave_sum_dpp(v);
@@ -140,7 +164,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
     __shared__ __attribute__((aligned(16))) float red[5][kMaxWaves];
     const int64_t m = blockIdx.x, K = a.K;
     const int waves = blockDim.x / 64;
-    clear_absent(red[0], 5, waves);
+    clear_absent(red[0], 4, J * waves > kMaxWaves ? waves : J * waves);  // sums
+    clear_absent(red[4], 1, waves);                                      // the maximum
     const Share<J, VEC> sh{(int)K, (int)threadIdx.x, (int)blockDim.x};
     const float inv_k = 1.0f / (float)K;
     const bool block = a.block != nullptr, token = a.gate_kind == kGateToken;
@@ -169,14 +194,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
         mean = 0.f;
         rstd = 1.f;
         if (s.kind == kNormNone) return;
-        float t = 0.f;
+        float t[J];
         if (s.kind == kNormLayer) {
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+                t[j] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t += x[j][e];
-            mean = group_sum(t, red0, waves) * inv_k;
-            t = 0.f;
+                for (int e = 0; e < 8; ++e) t[j] += x[j][e];
+            }
+            mean = group_sum_chunks(t, red0, waves) * inv_k;
         }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -184,10 +210,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = x[j][e] - mean;
             if (s.kind == kNormLayer) clear_past(j, sh, d);
+            t[j] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t = __builtin_fmaf(d[e], d[e], t);
+            for (int e = 0; e < 8; ++e) t[j] = __builtin_fmaf(d[e], d[e], t[j]);
         }
-        rstd = 1.0f / sqrtf(group_sum(t, red1, waves) * inv_k + s.eps);
+        rstd = 1.0f / sqrtf(group_sum_chunks(t, red1, waves) * inv_k + s.eps);
     };
 
     float v[J][8];  // h'

@@ -441,3 +441,19 @@ def test_gradient_against_differences(bl):
     slope = (loss(step) - loss(-step)) / (2 * step)
     terms = torch.cat([(getattr(r, k).cpu().double() * v).reshape(-1) for k, v in dirs.items()])
     assert abs(terms.sum() - slope) <= 1e-5 * terms.abs().sum()
+
+
+@pytest.mark.parametrize("K", [64, 1000, 2048, 4096, 5001, 8192, 11008])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_rows_do_not_depend_on_the_batch(bl, K, kind):
+    """A token's outputs, codes and statistics are the same bits alone, in a small
+    batch and in one that takes the many-row launch shape."""
+    c = Case(bl, 1024, K, "bf16", "bf16", pre=kind, post=kind, bias=kind == "layer", seed=K)
+    big = c.call(quant=True, stats=True)
+    for rows in (slice(0, 1), slice(5, 12), slice(0, 511)):
+        part = Case.__new__(Case)
+        part.__dict__.update(c.__dict__)
+        part.h, part.block = c.h[rows], c.block[rows]
+        r = part.call(quant=True, stats=True)
+        for k in ("h_out", "n", "xq", "scale", "stats"):
+            assert torch.equal(getattr(r, k), getattr(big, k)[rows]), (k, rows)
