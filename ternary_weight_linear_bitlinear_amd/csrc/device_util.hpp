@@ -115,6 +115,26 @@ __device__ __forceinline__ uint32_t quant4(float x0, float x1, float x2, float x
     return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
+// Sixteen activation codes at any address, as one (hardware-split) access.
+struct __attribute__((packed, aligned(1))) Bytes16 { int w[4]; };
+__device__ __forceinline__ v4i load16_any(const int8_t *p) {
+    const Bytes16 b = *reinterpret_cast<const Bytes16 *>(p);
+    return v4i{b.w[0], b.w[1], b.w[2], b.w[3]};
+}
+// Bytes s .. 15 of v moved to the front, zeros behind them (s >= 0; 16 and more: all zero).
+__device__ __forceinline__ v4i drop_bytes(v4i v, int s) {
+    uint32_t w[5] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3], 0u};
+#pragma unroll
+    for (int b = 2; b > 0; b /= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (s / 4) & b ? (i + b < 4 ? w[i + b] : 0u) : w[i];
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = s >= 16 ? 0 : (int)__builtin_amdgcn_alignbyte(w[i + 1], w[i], s & 3);
+    return r;
+}
+
 // Workgroup barrier for LDS hand-offs only: waits for this wave's LDS
 // operations (so its LDS writes are visible and its LDS reads have returned),
 // then s_barrier. Unlike __syncthreads() it does not wait for outstanding

@@ -45,7 +45,7 @@ constexpr int kXcds = 8;
 //            rows carry no padding codes: loads need no guard;
 //  kGuardedK K % 16 == 0 otherwise: the last k-tile's data past K is zeroed
 //            where it is consumed;
-//  kRaggedK  K % 16 != 0: activation rows are read byte-wise.
+//  kRaggedK  K % 16 != 0: activation rows are read in unaligned pieces.
 constexpr int kWholeK = 0, kGuardedK = 1, kRaggedK = 2;
 inline int gemm_k_mode(int layout, int64_t K) {
     if (K % 16 != 0) return kRaggedK;
@@ -353,7 +353,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     // (data past K in the last k-tile) read the same valid addresses and zero
     // what lies past K where it is consumed, so no branch or select splits the
     // load stream and the compiler keeps all of a tile's loads in flight. Rows
-    // that are not a multiple of 16 bytes load dwords (K % 4 == 0) or bytes.
+    // that are not a multiple of 16 bytes load unaligned pieces.
     auto load_tile = [&](int64_t kt, v4i *a_reg, uint4 *b_reg, auto guard_c) {
         constexpr bool G = decltype(guard_c)::value;
         if (!G) kt = kt < ktiles ? kt : ktiles - 1;
@@ -369,18 +369,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
                 // guarded tiles zero the chunks past K in store_a)
                 const int64_t mr = m < M ? m : M - 1;
                 a_reg[i] = *reinterpret_cast<const v4i *>(xq + mr * K + (k < K ? k : 0));
-            } else if (K % 4 == 0) {
-                // rows 4-byte aligned: four dword loads; dwords past K read
-                // the row's first one and are zeroed in store_a
+            } else if (K >= 16) {
+                // rows begin at any byte: a chunk that would run past the row's
+                // end reads the row's last 16 bytes instead, which store_a moves
+                // into place (100 x 5003 x 2001 against byte by byte: 2-bit 25.0 ->
+                // 11.6 us, base-3 67.8 -> 19.0 us; 300 tokens 38.9 -> 18.0 and 70.9 ->
+                // 21.6 us)
                 const int64_t mr = m < M ? m : M - 1;
-                const int32_t *p = reinterpret_cast<const int32_t *>(xq + mr * K);
-                v4i v;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int64_t kd = k + 4 * d;
-                    v[d] = p[(kd < K ? kd : 0) / 4];
-                }
-                a_reg[i] = v;
+                a_reg[i] = load16_any(xq + mr * K + (k < K - 16 ? k : K - 16));
             } else {
                 v4i v = {0, 0, 0, 0};
                 if (m < M && k < K) {
@@ -404,7 +400,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     };
 
     // Stage the activation registers of k-tile kt in LDS. Guarded tiles zero
-    // the chunks (dwords, for 4-byte rows) past K here, where the values are
+    // the chunks past K here, where the values are
     // consumed (a select at the load would make the compiler wait for it).
     auto store_a = [&](int8_t *As, const v4i *a_reg, int64_t kt, auto guard_c) {
         constexpr bool Z = decltype(guard_c)::value && EVEN_K;
@@ -418,11 +414,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
             if constexpr (Z) {
                 if (kb >= K) v = v4i{0, 0, 0, 0};
             }
-            if constexpr (KMODE == kRaggedK) {  // the dword path of load_tile
-                if (K % 4 == 0) {
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        if (kb + 4 * d >= K) v[d] = 0;
+            if constexpr (KMODE == kRaggedK) {
+                // (uniform: only the row's last k-tiles hold its end)
+                if (K >= 16 && (kt + 1) * C::BK > K) {
+                    const int64_t past = kb + 16 - K;
+                    v = drop_bytes(v, past > 0 ? (past < 16 ? (int)past : 16) : 0);
                 }
             }
             *reinterpret_cast<v4i *>(As + row * C::LDSK + col * 16) = v;

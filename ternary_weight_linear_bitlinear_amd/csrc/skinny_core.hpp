@@ -346,12 +346,17 @@ __device__ __forceinline__ void skinny_block(
                 wv[q][s] = load_unit<LAYOUT>(ok ? wrow[q] + unit * C::kUnitBytes : packed);
             }
     };
-    // chunks of K % 16 != 0 rows, byte by byte (zero past K)
+    // chunks of K % 16 != 0 rows: unaligned 16-byte pieces, the row's end byte by
+    // byte (zero past K)
     auto stage_bytes = [&](int64_t k0) {
         for (int q = threadIdx.x; q < chunks; q += kThreads) {
             const int t = q / kChunksPerTok, cc = q % kChunksPerTok;
             const int64_t k = k0 + cc * 16;
             const int8_t *src = xq + (int64_t)t * K;
+            if (k + 16 <= K) {
+                *reinterpret_cast<v4i *>(act + t * kActStride + cc * 16) = load16_any(src + k);
+                continue;
+            }
             uint32_t d[4] = {0u, 0u, 0u, 0u};
             for (int e = 0; e < 16; ++e)
                 if (k + e < K) d[e / 4] |= (uint32_t)(uint8_t)src[k + e] << (8 * (e % 4));
