@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import NamedTuple
 
@@ -401,8 +402,8 @@ def linear(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor, N: int, l
 # ---- bias, activation and residual in the epilogue; norms around a block ----
 # These calls check what the C ABI cannot see (shapes, types, devices, strides)
 # and raise BitLinearError for it as for the library's own refusals. They run on
-# the device of their first tensor and on its current stream unless `stream` is
-# given. The decode products take a few microseconds, so the checks are kept to
+# the device of their first tensor and its current stream, or (keyword `stream`)
+# with another stream made current. The decode products take a few microseconds, so the checks are kept to
 # one pass over each tensor's attributes and what depends on sizes alone is cached.
 _f32, _bf16 = torch.float32, torch.bfloat16
 _FLT_MAX = 3.4028234663852886e38
@@ -442,19 +443,29 @@ def _float(where: str, name: str, t: torch.Tensor):
     return dtype
 
 
-def _run(where: str, dev: int, stream, call, args) -> None:
-    """One library call on GPU `dev`, on its current stream unless one is given."""
+def _run(where: str, dev: int, call, args) -> None:
+    """One library call on GPU `dev` and its current stream."""
     if dev < 0:
         _refuse(where, "tensors are on the cpu")
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-                          else stream.cuda_stream)
+            status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        status = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-                      else stream.cuda_stream)
+        status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != BL_OK:
         raise BitLinearError(status, where)
+
+
+def _on_stream(call):
+    """`stream=` runs the call with that stream current, so that what it allocates
+    (outputs, workspace) belongs to the stream that the kernels run on."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on_stream
 
 
 def _one_of(where: str, name: str, v, table) -> int:
@@ -474,17 +485,24 @@ def _check_scale(where: str, v) -> None:
 @functools.lru_cache(maxsize=1024)
 def _segments(rows):
     """Row counts as the C table (never written), their number and their sum."""
-    rows = (rows,) if isinstance(rows, int) else rows
-    return _seg_table(rows)
+    return _seg_table((rows,) if isinstance(rows, int) else rows)
+
+
+def _rows_of(seg_rows):
+    """seg_rows as a key of _segments: a tuple of counts, or one count."""
+    try:
+        return operator.index(seg_rows)
+    except TypeError:
+        return tuple(seg_rows)
 
 
 _row_bytes = functools.lru_cache(maxsize=1024)(bitlinear_packed_row_bytes)
 
 
 def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act, residual,
-                      residual_scale, out_dtype, y, z, stream):
+                      residual_scale, out_dtype, y, z):
     lay = _one_of(where, "layout", layout, LAYOUTS)
-    table, nseg, N = _segments(seg_rows if isinstance(seg_rows, (int, tuple)) else tuple(seg_rows))
+    table, nseg, N = _segments(seg_rows if type(seg_rows) is int else _rows_of(seg_rows))
     if out_dtype is None:
         out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else _f32
     if out_dtype is not _f32 and out_dtype is not _bf16:
@@ -507,15 +525,16 @@ def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, la
             None if residual is None else _addr(where, "residual", residual, shape, out_dtype, dev),
             residual_scale, _addr(where, "z", z, shape, out_dtype, dev) if want_z else None,
             _addr(where, "y", y, shape, out_dtype, dev), BL_F32 if out_dtype is _f32 else BL_BF16)
-    _run(where, dev, stream, call, args)
+    _run(where, dev, call, args)
     return (y, z) if want_z else y
 
 
+@_on_stream
 def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tensor,
                                gammas: torch.Tensor, seg_rows, K: int, layout="2bit", bias=None,
                                act="none", residual=None, residual_scale: float = 1.0,
                                out_dtype=None, y: torch.Tensor | None = None,
-                               z: torch.Tensor | bool | None = None, stream=None):
+                               z: torch.Tensor | bool | None = None):
     """y = act(z) + residual_scale * residual with z = the product of
     bitlinear_forward (bitlinear_forward_segmented) + bias.
 
@@ -529,42 +548,43 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
     M, dev = xq.shape[0], xq.get_device()
     lead = (_addr(where, "xq", xq, (M, K), torch.int8, dev), _addr(where, "scale", scale, (M,), _f32, dev))
     return _product_epilogue(where, _lib.bitlinear_forward_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
-                             layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
+                             layout, bias, act, residual, residual_scale, out_dtype, y, z)
 
 
+@_on_stream
 def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
                               layout="2bit", bias=None, act="none", residual=None,
                               residual_scale: float = 1.0, out_dtype=None,
-                              y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None,
-                              stream=None):
+                              y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None):
     """bitlinear_forward_epilogue fused with the quantisation of x, M <= 4 tokens."""
     where = "bitlinear_linear_epilogue"
     shape, dtype, dev = _lead(where, "x", x)
     M, K = shape
     lead = (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16)
     return _product_epilogue(where, _lib.bitlinear_linear_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
-                             layout, bias, act, residual, residual_scale, out_dtype, y, z, stream)
+                             layout, bias, act, residual, residual_scale, out_dtype, y, z)
 
 
+@_on_stream
 def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
                     layout="2bit", bias=None, act="none", residual=None,
                     residual_scale: float = 1.0, out_dtype=None, y: torch.Tensor | None = None,
-                    z: torch.Tensor | bool | None = None, stream=None):
+                    z: torch.Tensor | bool | None = None):
     """``linear`` with bias, activation and residual: one fused launch for
     M <= 4, otherwise quantise then multiply."""
     if x.shape[0] <= FUSED_MAX_M:
         return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
-                                         out_dtype, y, z, stream)
+                                         out_dtype, y, z)
     where = "linear_epilogue"
     shape, dtype, dev = _lead(where, "x", x)
     M, K = shape
     xq = torch.empty(shape, dtype=torch.int8, device=x.device)
     scale = torch.empty(M, dtype=_f32, device=x.device)
-    _run(where, dev, stream, _lib.bitlinear_quant_acts,
+    _run(where, dev, _lib.bitlinear_quant_acts,
          (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16, M, K, xq.data_ptr(),
           scale.data_ptr()))
     return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, K, layout, bias, act, residual,
-                                      residual_scale, out_dtype, y, z, stream)
+                                      residual_scale, out_dtype, y, z)
 
 
 def _workspace(where: str, ws, need: int, t: torch.Tensor):
@@ -587,12 +607,13 @@ def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
     return int(_lib.bitlinear_epilogue_backward_workspace_bytes(M, N))
 
 
+@_on_stream
 def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, act="none",
                                 residual_scale: float = 1.0, out_dtype=None,
                                 grad_z: torch.Tensor | bool | None = True,
                                 grad_bias: torch.Tensor | bool | None = True,
                                 grad_residual: torch.Tensor | bool | None = None,
-                                workspace: torch.Tensor | None = None, stream=None) -> EpilogueGrads:
+                                workspace: torch.Tensor | None = None) -> EpilogueGrads:
     """Gradients of y = act(z) + residual_scale * residual, z = product + bias:
     grad_z [M, N] (out_dtype, grad_y's type by default), grad_bias [N] fp32,
     grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
@@ -625,7 +646,7 @@ def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, ac
             None if grad_bias is None else _addr(where, "grad_bias", grad_bias, (N,), _f32, dev),
             None if grad_residual is None else _addr(where, "grad_residual", grad_residual, shape, dtype, dev),
             ws, ws_bytes)
-    _run(where, dev, stream, _lib.bitlinear_epilogue_backward, args)
+    _run(where, dev, _lib.bitlinear_epilogue_backward, args)
     return EpilogueGrads(grad_z, grad_bias, grad_residual)
 
 
@@ -683,13 +704,14 @@ def _norm_args(where, shape, dev, x_dtype, pre, post, gate):
             BL_F32 if P is _f32 else BL_BF16)
 
 
+@_on_stream
 def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
                          pre: Norm | None = None, post: Norm | None = None,
                          gate: torch.Tensor | None = None, residual_scale: float = 1.0,
                          out_dtype=None, normed: bool = True, quant: bool = False,
                          h_out: torch.Tensor | None = None, n: torch.Tensor | None = None,
                          xq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
-                         stats: torch.Tensor | bool | None = None, stream=None) -> BlockNorm:
+                         stats: torch.Tensor | bool | None = None) -> BlockNorm:
     """h_out = residual_scale * h + gate * post(block) and n = pre(h_out), in one
     pass over h [M, K] and block [M, K].
 
@@ -733,7 +755,7 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
             None if xq is None else _addr(where, "xq", xq, shape, torch.int8, dev),
             None if scale is None else _addr(where, "scale", scale, (M,), _f32, dev),
             None if stats is None else _addr(where, "stats", stats, (M, 4), _f32, dev))
-    _run(where, dev, stream, _lib.bitlinear_block_norm, args)
+    _run(where, dev, _lib.bitlinear_block_norm, args)
     return BlockNorm(h if block is None else h_out, n, xq, scale, stats)
 
 
@@ -742,6 +764,7 @@ def bitlinear_block_norm_backward_workspace_bytes(M: int, K: int) -> int:
     return int(_lib.bitlinear_block_norm_backward_workspace_bytes(M, K))
 
 
+@_on_stream
 def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch.Tensor | None,
                                   h_out: torch.Tensor, block: torch.Tensor | None,
                                   stats: torch.Tensor, pre: Norm | None = None,
@@ -754,8 +777,7 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
                                   grad_post_bias: torch.Tensor | None = None,
                                   grad_pre_weight: torch.Tensor | None = None,
                                   grad_pre_bias: torch.Tensor | None = None,
-                                  workspace: torch.Tensor | None = None,
-                                  stream=None) -> BlockNormGrads:
+                                  workspace: torch.Tensor | None = None) -> BlockNormGrads:
     """Gradients of bitlinear_block_norm. h_out, stats: as that call returned
     them; grad_h_out: the gradient of h_out from its other uses (None: zero);
     grad_n: the gradient of n (None without pre), or of the quantised input
@@ -806,6 +828,6 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
             None if grad_pre_weight is None else _addr(where, "grad_pre_weight", grad_pre_weight, row, _f32, dev),
             None if grad_pre_bias is None else _addr(where, "grad_pre_bias", grad_pre_bias, row, _f32, dev),
             ws, ws_bytes)
-    _run(where, dev, stream, _lib.bitlinear_block_norm_backward, args)
+    _run(where, dev, _lib.bitlinear_block_norm_backward, args)
     return BlockNormGrads(grad_h, grad_block, grad_gate, grad_post_weight, grad_post_bias,
                           grad_pre_weight, grad_pre_bias)

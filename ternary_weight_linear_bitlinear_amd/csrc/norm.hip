@@ -160,9 +160,10 @@ __device__ __forceinline__ void load_params(const void *p, const void *q, int j,
 }
 
 template <typename HT, typename XT, typename PT, int J, bool VEC>
-__global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockNormArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockNormArgs a,
+                                                                    int64_t m0) {
     __shared__ __attribute__((aligned(16))) float red[5][kMaxWaves];
-    const int64_t m = blockIdx.x, K = a.K;
+    const int64_t m = m0 + blockIdx.x, K = a.K;
     const int waves = blockDim.x / 64;
     clear_absent(red[0], 4, J * waves > kMaxWaves ? waves : J * waves);  // sums
     clear_absent(red[4], 1, waves);                                      // the maximum
@@ -306,8 +307,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 // stays in the caches), the last pass writes. Every element is read and written
 // by one thread, and nothing is written before the last pass, so h_out may be h.
 template <typename HT, typename XT, typename PT>
-__global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNormArgs a) {
-    const int64_t m = blockIdx.x, K = a.K;
+__global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNormArgs a,
+                                                                   int64_t m0) {
+    const int64_t m = m0 + blockIdx.x, K = a.K;
     const HT *h = static_cast<const HT *>(a.h) + m * K;
     const XT *b = a.block ? static_cast<const XT *>(a.block) + m * K : nullptr;
     const XT *gt = a.gate_kind == kGateToken ? static_cast<const XT *>(a.gate) + m * K : nullptr;
@@ -616,8 +618,9 @@ struct GradRow {
 };
 
 template <typename HT, typename XT, typename NT, typename PT>
-__global__ __launch_bounds__(kThreads) void block_norm_grad_rows_kernel(const BlockNormGradArgs a) {
-    const int64_t m = blockIdx.x, K = a.K;
+__global__ __launch_bounds__(kThreads) void block_norm_grad_rows_kernel(const BlockNormGradArgs a,
+                                                                        int64_t m0) {
+    const int64_t m = m0 + blockIdx.x, K = a.K;
     const GradRow<HT, XT, NT, PT> r(a, m);
     const void *gc = a.gate_kind == kGateChannel ? a.gate : nullptr;
     float c1 = 0.f, c2 = 0.f, e1 = 0.f, e2 = 0.f;
@@ -715,6 +718,21 @@ int64_t grad_runs(int64_t M, int64_t K) {
 
 }  // namespace
 
+namespace {
+// One workgroup per row: launches of at most this many rows, since a grid holds
+// fewer than 2^32 threads in a dimension. launch(first row, rows).
+constexpr int64_t kLaunchRows = 1 << 21;
+template <typename F>
+hipError_t by_rows(int64_t M, F launch) {
+    for (int64_t m0 = 0; m0 < M; m0 += kLaunchRows) {
+        launch(m0, dim3((unsigned)(M - m0 < kLaunchRows ? M - m0 : kLaunchRows)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+}  // namespace
+
 hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
     return typed(a.h_dtype, [&](auto h) {
         return typed(a.x_dtype, [&](auto x) {
@@ -722,18 +740,18 @@ hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream) {
                 using HT = Pointee<decltype(h)>;
                 using XT = Pointee<decltype(x)>;
                 using PT = Pointee<decltype(p)>;
-                const dim3 grid((unsigned)a.M);
-                if (!holds_row(a.K)) {
-                    hipLaunchKernelGGL((block_norm_rows_kernel<HT, XT, PT>), grid, dim3(kThreads),
-                                       0, stream, a);
-                    return hipGetLastError();
-                }
+                if (!holds_row(a.K))
+                    return by_rows(a.M, [&](int64_t m0, dim3 grid) {
+                        hipLaunchKernelGGL((block_norm_rows_kernel<HT, XT, PT>), grid,
+                                           dim3(kThreads), 0, stream, a, m0);
+                    });
                 auto go = [&](auto j_c, auto vec_c) {
                     constexpr int J = decltype(j_c)::value;
                     const int64_t threads = ((a.K + 8 * J - 1) / (8 * J) + 63) / 64 * 64;
-                    hipLaunchKernelGGL((block_norm_kernel<HT, XT, PT, J, decltype(vec_c)::value>),
-                                       grid, dim3((unsigned)threads), 0, stream, a);
-                    return hipGetLastError();
+                    return by_rows(a.M, [&](int64_t m0, dim3 grid) {
+                        hipLaunchKernelGGL((block_norm_kernel<HT, XT, PT, J, decltype(vec_c)::value>),
+                                           grid, dim3((unsigned)threads), 0, stream, a, m0);
+                    });
                 };
                 auto chunks = [&](auto vec_c) {
                     if (a.K <= kRegElems && !(a.M >= kManyRows && a.K >= 2048))
@@ -786,9 +804,10 @@ hipError_t launch_block_norm_backward(const BlockNormGradArgs &a, hipStream_t st
                         };
                         return a.K % 8 == 0 ? chunks(std::true_type{}) : chunks(std::false_type{});
                     }
-                    hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>),
-                                       dim3((unsigned)a.M), dim3(kThreads), 0, stream, a);
-                    hipError_t e = hipGetLastError();
+                    hipError_t e = by_rows(a.M, [&](int64_t m0, dim3 grid) {
+                        hipLaunchKernelGGL((block_norm_grad_rows_kernel<HT, XT, NT, PT>), grid,
+                                           dim3(kThreads), 0, stream, a, m0);
+                    });
                     if (e != hipSuccess || !cols) return e;
                     hipLaunchKernelGGL((block_norm_grad_cols_kernel<HT, XT, NT, PT>),
                                        dim3((unsigned)((a.K + kThreads - 1) / kThreads), (unsigned)runs),

@@ -457,3 +457,26 @@ def test_rows_do_not_depend_on_the_batch(bl, K, kind):
         r = part.call(quant=True, stats=True)
         for k in ("h_out", "n", "xq", "scale", "stats"):
             assert torch.equal(getattr(r, k), getattr(big, k)[rows]), (k, rows)
+
+
+def test_more_rows_than_one_grid(bl):
+    """2^26 + 5 rows of 8 (more than 2^32 threads at one workgroup per row), and
+    2^24 rows of 4 backward: the rows around the launches' ends equal the same rows alone."""
+    M, K = (1 << 26) + 5, 8
+    h = torch.full((M, K), 0.5, dtype=BF16, device="cuda")
+    rows = torch.tensor([0, (1 << 21) - 1, 1 << 21, (1 << 26) - 1, 1 << 26, M - 1], device="cuda")
+    h[rows] = torch.randn(len(rows), K, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF16)
+    w = torch.linspace(0.5, 1.5, K, device="cuda")
+    big = bl.bitlinear_block_norm(h, pre=bl.Norm("rms", w)).n
+    assert torch.equal(big[rows], bl.bitlinear_block_norm(h[rows], pre=bl.Norm("rms", w)).n)
+    assert torch.equal(big[1000], bl.bitlinear_block_norm(h[1000:1001], pre=bl.Norm("rms", w)).n[0])
+    del big, h
+    M, K = 1 << 24, 4
+    h = torch.full((M, K), 0.5, device="cuda")
+    rows = torch.tensor([0, (1 << 21) - 1, 1 << 21, M - 1], device="cuda")
+    h[rows] = torch.randn(len(rows), K, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    norm = bl.Norm("rms", w[:K].contiguous())
+    st = bl.bitlinear_block_norm(h, pre=norm, stats=True).stats
+    big = bl.bitlinear_block_norm_backward(h, h, h, None, st, pre=norm).grad_h
+    assert torch.equal(big[rows], bl.bitlinear_block_norm_backward(h[rows], h[rows], h[rows], None, st[rows],
+                                                                   pre=norm).grad_h)

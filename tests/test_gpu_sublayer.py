@@ -183,3 +183,23 @@ def test_explicit_stream(bl):
     assert torch.equal(got.n, want.n) and torch.equal(got.h_out, want.h_out)
     assert torch.equal(y, bl.bitlinear_linear_epilogue(s.h[:2], *s.up, s.F, bias=s.up_bias, act="gelu"))
     assert torch.equal(r.grad_bias, bl.bitlinear_epilogue_backward(s.gy, s.h, "silu").grad_bias)
+
+
+def test_outputs_belong_to_the_given_stream(bl):
+    """With `stream`, outputs and workspaces come from that stream's memory: results
+    stay right while the current stream keeps freeing and refilling tensors of the
+    same sizes."""
+    s = Sublayer(bl, 512, 1024, 1032, seed=4)
+    want = bl.bitlinear_epilogue_backward(s.gy, s.h, "silu")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append(bl.bitlinear_epilogue_backward(s.gy, s.h, "silu", stream=st))
+        for _ in range(3):
+            torch.empty(512 * 1024, device="cuda").fill_(float("nan"))
+            torch.empty(bl.bitlinear_epilogue_backward_workspace_bytes(512, 1024), dtype=torch.uint8,
+                        device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    for r in got:
+        assert torch.equal(r.grad_z, want.grad_z) and torch.equal(r.grad_bias, want.grad_bias)
