@@ -656,7 +656,7 @@ def main():
     if os.path.exists(counters):
         with open(counters) as f:
             c = json.load(f)
-        src = os.path.join(ROOT, "ternary_weight_linear_bitlinear_amd", "csrc", "skinny.hip")
+        src = os.path.join(ROOT, "ternary_weight_linear_bitlinear_amd", "csrc", "skinny_core.hpp")
         if not os.path.exists(src):
             src = None
         sha = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16] if src else None
