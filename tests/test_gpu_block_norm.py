@@ -480,3 +480,11 @@ def test_more_rows_than_one_grid(bl):
     big = bl.bitlinear_block_norm_backward(h, h, h, None, st, pre=norm).grad_h
     assert torch.equal(big[rows], bl.bitlinear_block_norm_backward(h[rows], h[rows], h[rows], None, st[rows],
                                                                    pre=norm).grad_h)
+
+
+@pytest.mark.parametrize("K", [4104, 6000, 6001, 8185])
+@pytest.mark.parametrize("kind,gate", [("layer", "token"), ("layer", "channel"), ("rms", "token")])
+def test_backward_two_chunks(bl, K, kind, gate):
+    """Rows of two chunks per thread, whose parameters lie in LDS."""
+    c = Case(bl, 7, K, "f32", "bf16", pre=kind, post=kind, gate=gate, bias=kind == "layer", scale=0.5, seed=K)
+    check_backward(c, run_backward(c, BF16))
