@@ -402,8 +402,9 @@ def linear(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor, N: int, l
 # ---- bias, activation and residual in the epilogue; norms around a block ----
 # These calls check what the C ABI cannot see (shapes, types, devices, strides)
 # and raise BitLinearError for it as for the library's own refusals. They run on
-# the device of their first tensor and its current stream, or (keyword `stream`)
-# with another stream made current. The decode products take a few microseconds, so the checks are kept to
+# the device of their first tensor and its current stream; `stream` makes another
+# one current first, so that what a call allocates (outputs, workspace) belongs to
+# the stream that its kernels run on. The decode products take a few microseconds, so the checks are kept to
 # one pass over each tensor's attributes and what depends on sizes alone is cached.
 _f32, _bf16 = torch.float32, torch.bfloat16
 _FLT_MAX = 3.4028234663852886e38
@@ -429,11 +430,13 @@ def _addr(where: str, name: str, t: torch.Tensor, shape, dtype, dev: int) -> int
 
 
 def _lead(where: str, name: str, t: torch.Tensor):
-    """Shape, type and GPU of the tensor that the others have to match."""
+    """Shape, type, GPU and address of the tensor that the others have to match."""
     dtype, shape = t.dtype, t.shape
     if (dtype is not _f32 and dtype is not _bf16) or len(shape) != 2:
         _refuse(where, f"{name} is {dtype} of shape {tuple(shape)}")
-    return shape, dtype, t.get_device()
+    if not t.is_contiguous():
+        _refuse(where, f"{name} is not contiguous")
+    return shape, dtype, t.get_device(), t.data_ptr()
 
 
 def _float(where: str, name: str, t: torch.Tensor):
@@ -454,18 +457,6 @@ def _run(where: str, dev: int, call, args) -> None:
         status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != BL_OK:
         raise BitLinearError(status, where)
-
-
-def _on_stream(call):
-    """`stream=` runs the call with that stream current, so that what it allocates
-    (outputs, workspace) belongs to the stream that the kernels run on."""
-    @functools.wraps(call)
-    def on_stream(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return on_stream
 
 
 def _one_of(where: str, name: str, v, table) -> int:
@@ -490,6 +481,8 @@ def _segments(rows):
 
 def _rows_of(seg_rows):
     """seg_rows as a key of _segments: a tuple of counts, or one count."""
+    if isinstance(seg_rows, (list, tuple)):
+        return tuple(seg_rows)
     try:
         return operator.index(seg_rows)
     except TypeError:
@@ -509,10 +502,10 @@ def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, la
         _refuse(where, f"out_dtype is {out_dtype}")
     shape = (M, N)
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=packed.device)
+        y = torch.empty(M, N, dtype=out_dtype, device=packed.device)
     want_z = z is not None and z is not False
     if z is True:
-        z = torch.empty(shape, dtype=out_dtype, device=packed.device)
+        z = torch.empty(M, N, dtype=out_dtype, device=packed.device)
     if (gammas.dtype is not _f32 or gammas.numel() < nseg or gammas.get_device() != dev
             or not gammas.is_contiguous()):
         _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for {nseg} segments, "
@@ -529,12 +522,12 @@ def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, la
     return (y, z) if want_z else y
 
 
-@_on_stream
 def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tensor,
                                gammas: torch.Tensor, seg_rows, K: int, layout="2bit", bias=None,
                                act="none", residual=None, residual_scale: float = 1.0,
                                out_dtype=None, y: torch.Tensor | None = None,
-                               z: torch.Tensor | bool | None = None):
+                               z: torch.Tensor | bool | None = None,
+                               stream=None):
     """y = act(z) + residual_scale * residual with z = the product of
     bitlinear_forward (bitlinear_forward_segmented) + bias.
 
@@ -542,6 +535,10 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
     residual may be y itself. out_dtype defaults to y's, then residual's type,
     then fp32; y, z and residual share it. Returns y, or (y, z) when z is
     requested."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, K, layout, bias, act, residual,
+                                              residual_scale, out_dtype, y, z)
     where = "bitlinear_forward_epilogue"
     if xq.dim() != 2:
         _refuse(where, f"xq has shape {tuple(xq.shape)}")
@@ -551,38 +548,43 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
                              layout, bias, act, residual, residual_scale, out_dtype, y, z)
 
 
-@_on_stream
 def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
                               layout="2bit", bias=None, act="none", residual=None,
                               residual_scale: float = 1.0, out_dtype=None,
-                              y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None):
+                              y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None,
+                              stream=None):
     """bitlinear_forward_epilogue fused with the quantisation of x, M <= 4 tokens."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual,
+                                             residual_scale, out_dtype, y, z)
     where = "bitlinear_linear_epilogue"
-    shape, dtype, dev = _lead(where, "x", x)
-    M, K = shape
-    lead = (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16)
+    (M, K), dtype, dev, x_at = _lead(where, "x", x)
+    lead = (x_at, BL_F32 if dtype is _f32 else BL_BF16)
     return _product_epilogue(where, _lib.bitlinear_linear_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
                              layout, bias, act, residual, residual_scale, out_dtype, y, z)
 
 
-@_on_stream
 def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, seg_rows,
                     layout="2bit", bias=None, act="none", residual=None,
                     residual_scale: float = 1.0, out_dtype=None, y: torch.Tensor | None = None,
-                    z: torch.Tensor | bool | None = None):
+                    z: torch.Tensor | bool | None = None,
+                    stream=None):
     """``linear`` with bias, activation and residual: one fused launch for
     M <= 4, otherwise quantise then multiply."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
+                                   out_dtype, y, z)
     if x.shape[0] <= FUSED_MAX_M:
         return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
                                          out_dtype, y, z)
     where = "linear_epilogue"
-    shape, dtype, dev = _lead(where, "x", x)
-    M, K = shape
-    xq = torch.empty(shape, dtype=torch.int8, device=x.device)
+    (M, K), dtype, dev, x_at = _lead(where, "x", x)
+    xq = torch.empty(M, K, dtype=torch.int8, device=x.device)
     scale = torch.empty(M, dtype=_f32, device=x.device)
     _run(where, dev, _lib.bitlinear_quant_acts,
-         (_addr(where, "x", x, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16, M, K, xq.data_ptr(),
-          scale.data_ptr()))
+         (x_at, BL_F32 if dtype is _f32 else BL_BF16, M, K, xq.data_ptr(), scale.data_ptr()))
     return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, K, layout, bias, act, residual,
                                       residual_scale, out_dtype, y, z)
 
@@ -607,19 +609,23 @@ def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
     return int(_lib.bitlinear_epilogue_backward_workspace_bytes(M, N))
 
 
-@_on_stream
 def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, act="none",
                                 residual_scale: float = 1.0, out_dtype=None,
                                 grad_z: torch.Tensor | bool | None = True,
                                 grad_bias: torch.Tensor | bool | None = True,
                                 grad_residual: torch.Tensor | bool | None = None,
-                                workspace: torch.Tensor | None = None) -> EpilogueGrads:
+                                workspace: torch.Tensor | None = None,
+                                stream=None) -> EpilogueGrads:
     """Gradients of y = act(z) + residual_scale * residual, z = product + bias:
     grad_z [M, N] (out_dtype, grad_y's type by default), grad_bias [N] fp32,
     grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
     None (leave out). z may be None for act "none"."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitlinear_epilogue_backward(grad_y, z, act, residual_scale, out_dtype, grad_z, grad_bias,
+                                               grad_residual, workspace)
     where = "bitlinear_epilogue_backward"
-    shape, dtype, dev = _lead(where, "grad_y", grad_y)
+    shape, dtype, dev, gy_at = _lead(where, "grad_y", grad_y)
     M, N = shape
     own = grad_z is not None and grad_z is not True and grad_z is not False
     if out_dtype is None:
@@ -627,19 +633,19 @@ def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, ac
     if out_dtype is not _f32 and out_dtype is not _bf16:
         _refuse(where, f"out_dtype is {out_dtype}")
     if not own:
-        grad_z = torch.empty(shape, dtype=out_dtype, device=grad_y.device) if grad_z else None
+        grad_z = torch.empty(M, N, dtype=out_dtype, device=grad_y.device) if grad_z else None
     if grad_bias is True:
         grad_bias = torch.empty(N, dtype=_f32, device=grad_y.device)
     elif grad_bias is False:
         grad_bias = None
     if grad_residual is True:
-        grad_residual = torch.empty(shape, dtype=dtype, device=grad_y.device)
+        grad_residual = torch.empty_like(grad_y)
     elif grad_residual is False:
         grad_residual = None
     _check_scale(where, residual_scale)
     need = bitlinear_epilogue_backward_workspace_bytes(M, N) if grad_bias is not None else 0
     hold, ws, ws_bytes = (None, None, 0) if need == 0 else _workspace(where, workspace, need, grad_y)
-    args = (_addr(where, "grad_y", grad_y, shape, dtype, dev), BL_F32 if dtype is _f32 else BL_BF16,
+    args = (gy_at, BL_F32 if dtype is _f32 else BL_BF16,
             None if z is None else _addr(where, "z", z, shape, _float(where, "z", z), dev),
             BL_F32 if z is None else _DTYPES[z.dtype], _one_of(where, "act", act, ACTS), residual_scale, M, N,
             None if grad_z is None else _addr(where, "grad_z", grad_z, shape, out_dtype, dev), _DTYPES[out_dtype],
@@ -704,14 +710,14 @@ def _norm_args(where, shape, dev, x_dtype, pre, post, gate):
             BL_F32 if P is _f32 else BL_BF16)
 
 
-@_on_stream
 def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
                          pre: Norm | None = None, post: Norm | None = None,
                          gate: torch.Tensor | None = None, residual_scale: float = 1.0,
                          out_dtype=None, normed: bool = True, quant: bool = False,
                          h_out: torch.Tensor | None = None, n: torch.Tensor | None = None,
                          xq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
-                         stats: torch.Tensor | bool | None = None) -> BlockNorm:
+                         stats: torch.Tensor | bool | None = None,
+                         stream=None) -> BlockNorm:
     """h_out = residual_scale * h + gate * post(block) and n = pre(h_out), in one
     pass over h [M, K] and block [M, K].
 
@@ -720,8 +726,12 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
     default); normed=False leaves it out. quant: also the INT8 codes and scale of
     n, as bitlinear_quant_acts(n in fp32). stats (a buffer or True): what the
     backward call needs. h_out may be h."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitlinear_block_norm(h, block, pre, post, gate, residual_scale, out_dtype, normed, quant, h_out,
+                                        n, xq, scale, stats)
     where = "bitlinear_block_norm"
-    shape, H, dev = _lead(where, "h", h)
+    shape, H, dev, h_at = _lead(where, "h", h)
     M, K = shape
     if block is not None:
         X = _float(where, "block", block)
@@ -731,23 +741,23 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
         _refuse(where, f"block is {X}, out_dtype {out_dtype}")
     post_a, pre_a, P = _norm_args(where, shape, dev, X, pre, post, gate)
     if block is not None and h_out is None:
-        h_out = torch.empty(shape, dtype=H, device=h.device)
+        h_out = torch.empty_like(h)
     if pre is None or not normed:
         if n is not None:
             _refuse(where, "n is given without a norm that writes it")
     elif n is None:
-        n = torch.empty(shape, dtype=X, device=h.device)
+        n = torch.empty(M, K, dtype=X, device=h.device)
     if quant or xq is not None or scale is not None:
         if xq is None:
-            xq = torch.empty(shape, dtype=torch.int8, device=h.device)
+            xq = torch.empty(M, K, dtype=torch.int8, device=h.device)
         if scale is None:
             scale = torch.empty(M, dtype=_f32, device=h.device)
     if stats is True:
-        stats = torch.empty((M, 4), dtype=_f32, device=h.device)
+        stats = torch.empty(M, 4, dtype=_f32, device=h.device)
     elif stats is False:
         stats = None
     _check_scale(where, residual_scale)
-    args = (_addr(where, "h", h, shape, H, dev), BL_F32 if H is _f32 else BL_BF16,
+    args = (h_at, BL_F32 if H is _f32 else BL_BF16,
             None if block is None else _addr(where, "block", block, shape, X, dev),
             BL_F32 if X is _f32 else BL_BF16, residual_scale, *post_a, *pre_a, P, M, K,
             None if h_out is None else _addr(where, "h_out", h_out, shape, H, dev),
@@ -759,12 +769,22 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
     return BlockNorm(h if block is None else h_out, n, xq, scale, stats)
 
 
+def _param_grad(where, name, t, p, row, dev):
+    """A [K] parameter gradient and its address: the buffer t, a new one where there
+    is a parameter p, or none."""
+    if t is not None:
+        return t, _addr(where, name, t, row, _f32, dev)
+    if p is None:
+        return None, None
+    t = torch.empty(row[0], dtype=_f32, device=p.device)
+    return t, t.data_ptr()
+
+
 @functools.lru_cache(maxsize=1024)
 def bitlinear_block_norm_backward_workspace_bytes(M: int, K: int) -> int:
     return int(_lib.bitlinear_block_norm_backward_workspace_bytes(M, K))
 
 
-@_on_stream
 def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch.Tensor | None,
                                   h_out: torch.Tensor, block: torch.Tensor | None,
                                   stats: torch.Tensor, pre: Norm | None = None,
@@ -777,57 +797,59 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
                                   grad_post_bias: torch.Tensor | None = None,
                                   grad_pre_weight: torch.Tensor | None = None,
                                   grad_pre_bias: torch.Tensor | None = None,
-                                  workspace: torch.Tensor | None = None) -> BlockNormGrads:
+                                  workspace: torch.Tensor | None = None,
+                                  stream=None) -> BlockNormGrads:
     """Gradients of bitlinear_block_norm. h_out, stats: as that call returned
     them; grad_h_out: the gradient of h_out from its other uses (None: zero);
     grad_n: the gradient of n (None without pre), or of the quantised input
     (straight-through). Parameter gradients are fp32 [K] (a gate per token: [M, K]
-    of block's type); params=False leaves out those that no buffer is given for.
-    New [K] gradients of one call share one allocation."""
+    of block's type); params=False leaves out those that no buffer is given for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitlinear_block_norm_backward(grad_h_out, grad_n, h_out, block, stats, pre, post, gate,
+                                                 residual_scale, params, grad_h, grad_block, grad_gate,
+                                                 grad_post_weight, grad_post_bias, grad_pre_weight, grad_pre_bias,
+                                                 workspace)
     where = "bitlinear_block_norm_backward"
-    shape, H, dev = _lead(where, "h_out", h_out)
+    shape, H, dev, h_at = _lead(where, "h_out", h_out)
     M, K = shape
     row = shape[1:]
     X = H if block is None else _float(where, "block", block)
     post_a, pre_a, P = _norm_args(where, shape, dev, X, pre, post, gate)
     token = post_a[1] == BL_GATE_TOKEN
     if grad_h is None:
-        grad_h = torch.empty(shape, dtype=H, device=h_out.device)
+        grad_h = torch.empty_like(h_out)
     if grad_block is None and block is not None:
-        grad_block = torch.empty(shape, dtype=X, device=h_out.device)
-    if params:
-        # what has a parameter and no buffer: rows of one tensor, each at a 16-byte boundary
-        rows = torch.empty((5, (K + 3) & ~3), dtype=_f32, device=h_out.device)
-        rows = iter((rows if K % 4 == 0 else rows[:, :K]).unbind())
-        if post is not None:
-            if grad_post_weight is None and post.weight is not None:
-                grad_post_weight = next(rows)
-            if grad_post_bias is None and post.bias is not None:
-                grad_post_bias = next(rows)
-        if pre is not None:
-            if grad_pre_weight is None and pre.weight is not None:
-                grad_pre_weight = next(rows)
-            if grad_pre_bias is None and pre.bias is not None:
-                grad_pre_bias = next(rows)
-        if grad_gate is None and gate is not None:
-            grad_gate = torch.empty(shape, dtype=X, device=h_out.device) if token else next(rows)
+        grad_block = torch.empty_like(block)
+    qw = qb = pw = pb = None
+    if post is not None and params:
+        _, qw, qb, _ = post
+    if pre is not None and params:
+        _, pw, pb, _ = pre
+    grad_post_weight, qw = _param_grad(where, "grad_post_weight", grad_post_weight, qw, row, dev)
+    grad_post_bias, qb = _param_grad(where, "grad_post_bias", grad_post_bias, qb, row, dev)
+    grad_pre_weight, pw = _param_grad(where, "grad_pre_weight", grad_pre_weight, pw, row, dev)
+    grad_pre_bias, pb = _param_grad(where, "grad_pre_bias", grad_pre_bias, pb, row, dev)
+    if not token:
+        grad_gate, gate_p = _param_grad(where, "grad_gate", grad_gate, gate if params else None, row, dev)
+    elif grad_gate is not None:
+        gate_p = _addr(where, "grad_gate", grad_gate, shape, X, dev)
+    elif params:
+        grad_gate = torch.empty_like(gate)
+        gate_p = grad_gate.data_ptr()
+    else:
+        gate_p = None
     _check_scale(where, residual_scale)
     hold, ws, ws_bytes = _workspace(where, workspace, bitlinear_block_norm_backward_workspace_bytes(M, K), h_out)
     args = (None if grad_h_out is None else _addr(where, "grad_h_out", grad_h_out, shape, H, dev),
             None if grad_n is None else _addr(where, "grad_n", grad_n, shape, _float(where, "grad_n", grad_n), dev),
             BL_F32 if grad_n is None else _DTYPES[grad_n.dtype],
-            _addr(where, "h_out", h_out, shape, H, dev), BL_F32 if H is _f32 else BL_BF16,
+            h_at, BL_F32 if H is _f32 else BL_BF16,
             None if block is None else _addr(where, "block", block, shape, X, dev),
             BL_F32 if X is _f32 else BL_BF16, _addr(where, "stats", stats, (M, 4), _f32, dev), residual_scale,
             *post_a[:5], *pre_a[:2], P, M, K, _addr(where, "grad_h", grad_h, shape, H, dev),
             None if grad_block is None else _addr(where, "grad_block", grad_block, shape, X, dev),
-            None if grad_gate is None else _addr(where, "grad_gate", grad_gate, shape if token else row,
-                                                 X if token else _f32, dev),
-            None if grad_post_weight is None else _addr(where, "grad_post_weight", grad_post_weight, row, _f32, dev),
-            None if grad_post_bias is None else _addr(where, "grad_post_bias", grad_post_bias, row, _f32, dev),
-            None if grad_pre_weight is None else _addr(where, "grad_pre_weight", grad_pre_weight, row, _f32, dev),
-            None if grad_pre_bias is None else _addr(where, "grad_pre_bias", grad_pre_bias, row, _f32, dev),
-            ws, ws_bytes)
+            gate_p, qw, qb, pw, pb, ws, ws_bytes)
     _run(where, dev, _lib.bitlinear_block_norm_backward, args)
     return BlockNormGrads(grad_h, grad_block, grad_gate, grad_post_weight, grad_post_bias,
                           grad_pre_weight, grad_pre_bias)
