@@ -404,8 +404,9 @@ def linear(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor, N: int, l
 # and raise BitLinearError for it as for the library's own refusals. They run on
 # the device of their first tensor and its current stream; `stream` makes another
 # one current first, so that what a call allocates (outputs, workspace) belongs to
-# the stream that its kernels run on. The decode products take a few microseconds, so the checks are kept to
-# one pass over each tensor's attributes and what depends on sizes alone is cached.
+# the stream that its kernels run on. The decode products take a few microseconds,
+# so the checks are kept to one pass over each tensor's attributes and what depends
+# on sizes alone is cached.
 _f32, _bf16 = torch.float32, torch.bfloat16
 _FLT_MAX = 3.4028234663852886e38
 
@@ -444,6 +445,13 @@ def _float(where: str, name: str, t: torch.Tensor):
     if dtype is not _f32 and dtype is not _bf16:
         _refuse(where, f"{name} is {dtype}")
     return dtype
+
+
+def _on(where: str, stream, t: torch.Tensor):
+    """The context that makes `stream`, one of t's GPU, the current one."""
+    if stream.device != t.device:
+        _refuse(where, f"the stream is of {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _run(where: str, dev: int, call, args) -> None:
@@ -536,7 +544,7 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
     then fp32; y, z and residual share it. Returns y, or (y, z) when z is
     requested."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("bitlinear_forward_epilogue", stream, xq):
             return bitlinear_forward_epilogue(xq, scale, packed, gammas, seg_rows, K, layout, bias, act, residual,
                                               residual_scale, out_dtype, y, z)
     where = "bitlinear_forward_epilogue"
@@ -555,7 +563,7 @@ def bitlinear_linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: tor
                               stream=None):
     """bitlinear_forward_epilogue fused with the quantisation of x, M <= 4 tokens."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("bitlinear_linear_epilogue", stream, x):
             return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual,
                                              residual_scale, out_dtype, y, z)
     where = "bitlinear_linear_epilogue"
@@ -573,10 +581,10 @@ def linear_epilogue(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor,
     """``linear`` with bias, activation and residual: one fused launch for
     M <= 4, otherwise quantise then multiply."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("linear_epilogue", stream, x):
             return linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
                                    out_dtype, y, z)
-    if x.shape[0] <= FUSED_MAX_M:
+    if x.dim() != 2 or x.shape[0] <= FUSED_MAX_M:
         return bitlinear_linear_epilogue(x, packed, gammas, seg_rows, layout, bias, act, residual, residual_scale,
                                          out_dtype, y, z)
     where = "linear_epilogue"
@@ -621,7 +629,7 @@ def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, ac
     grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
     None (leave out). z may be None for act "none"."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("bitlinear_epilogue_backward", stream, grad_y):
             return bitlinear_epilogue_backward(grad_y, z, act, residual_scale, out_dtype, grad_z, grad_bias,
                                                grad_residual, workspace)
     where = "bitlinear_epilogue_backward"
@@ -727,7 +735,7 @@ def bitlinear_block_norm(h: torch.Tensor, block: torch.Tensor | None = None,
     n, as bitlinear_quant_acts(n in fp32). stats (a buffer or True): what the
     backward call needs. h_out may be h."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("bitlinear_block_norm", stream, h):
             return bitlinear_block_norm(h, block, pre, post, gate, residual_scale, out_dtype, normed, quant, h_out,
                                         n, xq, scale, stats)
     where = "bitlinear_block_norm"
@@ -805,7 +813,7 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
     (straight-through). Parameter gradients are fp32 [K] (a gate per token: [M, K]
     of block's type); params=False leaves out those that no buffer is given for."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on("bitlinear_block_norm_backward", stream, h_out):
             return bitlinear_block_norm_backward(grad_h_out, grad_n, h_out, block, stats, pre, post, gate,
                                                  residual_scale, params, grad_h, grad_block, grad_gate,
                                                  grad_post_weight, grad_post_bias, grad_pre_weight, grad_pre_bias,

@@ -218,3 +218,24 @@ def test_binding_refuses_epilogue_backward_arguments(bl, kw, word):
     a = dict(grad_y=torch.ones(5, 8), z=torch.ones(5, 8), act="gelu")
     with pytest.raises(bl.BitLinearError, match=word):
         bl.bitlinear_epilogue_backward(**{**a, **kw})
+
+
+def test_binding_refuses_a_stream_of_another_device(bl):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    st, t, h = Stream(), tensors(), torch.ones(5, 64)
+    w = (t["packed"], t["gammas"], 8)
+    for f in (lambda: bl.bitlinear_forward_epilogue(**t, stream=st), lambda: bl.bitlinear_linear_epilogue(h[:2], *w, stream=st),
+              lambda: bl.linear_epilogue(h, *w, stream=st), lambda: bl.bitlinear_epilogue_backward(h, h, "silu", stream=st),
+              lambda: bl.bitlinear_block_norm(h, pre=bl.Norm(), stream=st),
+              lambda: bl.bitlinear_block_norm_backward(None, h, h, None, torch.ones(5, 4), pre=bl.Norm(), stream=st)):
+        with pytest.raises(bl.BitLinearError, match="stream is of cuda:1"):
+            f()
+
+
+@pytest.mark.parametrize("shape", [(), (64,), (1, 5, 64)])
+def test_binding_refuses_activations_of_other_ranks(bl, shape):
+    t = tensors()
+    for f in (bl.linear_epilogue, bl.bitlinear_linear_epilogue):
+        with pytest.raises(bl.BitLinearError, match="x is"):
+            f(torch.ones(shape), t["packed"], t["gammas"], 8)
