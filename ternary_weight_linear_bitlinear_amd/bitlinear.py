@@ -488,13 +488,14 @@ def _segments(rows):
 
 
 def _rows_of(seg_rows):
-    """seg_rows as a key of _segments: a tuple of counts, or one count."""
-    if isinstance(seg_rows, (list, tuple)):
-        return tuple(seg_rows)
-    try:
-        return operator.index(seg_rows)
-    except TypeError:
-        return tuple(seg_rows)
+    """seg_rows as a key of _segments: a tuple of counts, or one count, as plain
+    numbers (a tensor would be a key by its identity, whatever it holds)."""
+    if not isinstance(seg_rows, (list, tuple)):
+        try:
+            return operator.index(seg_rows)
+        except TypeError:
+            pass
+    return tuple([int(r) for r in seg_rows])
 
 
 _row_bytes = functools.lru_cache(maxsize=1024)(bitlinear_packed_row_bytes)

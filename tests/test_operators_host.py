@@ -239,3 +239,16 @@ def test_binding_refuses_activations_of_other_ranks(bl, shape):
     for f in (bl.linear_epilogue, bl.bitlinear_linear_epilogue):
         with pytest.raises(bl.BitLinearError, match="x is"):
             f(torch.ones(shape), t["packed"], t["gammas"], 8)
+
+
+def test_segment_rows_are_read_at_each_call(bl):
+    """Row counts held in 0-d tensors are taken as the numbers they are at the call:
+    a changed count is a changed stack (refused here for its packed rows)."""
+    rows = [torch.tensor(4), torch.tensor(4)]
+    args = {**tensors(), "gammas": torch.ones(2), "seg_rows": rows}
+    for more, word in ((0, "cpu"), (1, "packed")):
+        rows[0] += more
+        with pytest.raises(bl.BitLinearError, match=word):
+            bl.bitlinear_forward_epilogue(**args)
+        with pytest.raises(bl.BitLinearError, match=word):
+            bl.bitlinear_linear_epilogue(torch.ones(2, 64), args["packed"], args["gammas"], tuple(rows))
