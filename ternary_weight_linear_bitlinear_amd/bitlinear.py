@@ -553,6 +553,7 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
         _refuse(where, f"xq has shape {tuple(xq.shape)}")
     M, dev = xq.shape[0], xq.get_device()
     lead = (_addr(where, "xq", xq, (M, K), torch.int8, dev), _addr(where, "scale", scale, (M,), _f32, dev))
+    K = xq.shape[1]
     return _product_epilogue(where, _lib.bitlinear_forward_epilogue, lead, M, K, dev, packed, gammas, seg_rows,
                              layout, bias, act, residual, residual_scale, out_dtype, y, z)
 

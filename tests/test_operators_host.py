@@ -252,3 +252,13 @@ def test_segment_rows_are_read_at_each_call(bl):
             bl.bitlinear_forward_epilogue(**args)
         with pytest.raises(bl.BitLinearError, match=word):
             bl.bitlinear_linear_epilogue(torch.ones(2, 64), args["packed"], args["gammas"], tuple(rows))
+
+
+def test_row_bytes_are_those_of_the_call(bl):
+    """K held in a 0-d tensor is the number that it is at the call: packed rows of
+    another K are refused."""
+    K = torch.tensor(64)
+    for k, word in ((64, "cpu"), (128, "packed")):
+        K.fill_(k)
+        with pytest.raises(bl.BitLinearError, match=word):
+            bl.bitlinear_forward_epilogue(**{**tensors(), "xq": torch.zeros(5, k, dtype=torch.int8), "K": K})
