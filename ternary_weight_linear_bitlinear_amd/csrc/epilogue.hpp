@@ -7,6 +7,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "activation.hpp"
 #include "bl_internal.hpp"
 #include "device_util.hpp"
@@ -151,6 +153,11 @@ struct Epilogue {
     }
 #endif
 };
+
+// How a product's kernel takes y: the plain epilogue never reads what it writes,
+// the extended one may be given y as its residual.
+template <typename YT, typename E>
+using OutPtr = std::conditional_t<E::kActive, YT *, YT *__restrict__>;
 
 template <typename YT>
 Epilogue<YT> make_epilogue(const EpilogueArgs &a) {

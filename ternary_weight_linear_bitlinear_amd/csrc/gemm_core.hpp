@@ -300,7 +300,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     const GammaMap &gm = g.gm;
     const int64_t M = g.M, N = g.N, K = g.K, rb = g.rb, ldy = g.ldy;
     const int tiles_n = g.tiles_n;
-    YT *__restrict__ y = g.y;
+    const OutPtr<YT, E> y = g.y;
     int32_t *__restrict__ acc_out = g.acc_out;
 
     int tr = t / tiles_n, tc = t % tiles_n;
@@ -827,7 +827,7 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
     const GammaMap &gm = g.gm;
     const int64_t M = g.M, K = g.K, rb = g.rb, ldy = g.ldy;
     const int tiles_n = g.tiles_n;
-    YT *__restrict__ y = g.y;
+    const OutPtr<YT, E> y = g.y;
     int32_t *__restrict__ acc_out = g.acc_out;
 
     int tr = t / tiles_n, tc = t % tiles_n;

@@ -275,7 +275,7 @@ template <int LAYOUT, int KS, int NSS, int RG, int MAXM, bool MR, typename YT, t
 __device__ __forceinline__ void skinny_block(
     const int8_t *__restrict__ xq, const float *__restrict__ scale,
     const uint8_t *__restrict__ packed, const GammaMap &gm, int M, int64_t N,
-    int64_t K, int64_t rb, YT *__restrict__ y, int32_t *__restrict__ acc_out, const E &ep) {
+    int64_t K, int64_t rb, OutPtr<YT, E> y, int32_t *__restrict__ acc_out, const E &ep) {
     using C = SkinnyCfg<LAYOUT>;
     constexpr int kThreads = 64 * KS;
     constexpr int kRoundUnits = KS * NSS * 4;                 // units per round
@@ -516,7 +516,7 @@ template <int LAYOUT, int KS, int NSS, int RG, int MAXM, bool MR, typename YT>
 __global__ __launch_bounds__(64 * KS) void skinny_epilogue_kernel(
     const int8_t *__restrict__ xq, const float *__restrict__ scale,
     const uint8_t *__restrict__ packed, const GammaMap gm, int M, int64_t N,
-    int64_t K, int64_t rb, YT *__restrict__ y, const Epilogue<YT> ep) {
+    int64_t K, int64_t rb, YT *y, const Epilogue<YT> ep) {
     skinny_block<LAYOUT, KS, NSS, RG, MAXM, MR, YT>(xq, scale, packed, gm, M, N, K, rb, y, nullptr,
                                                     ep);
 }
@@ -615,7 +615,7 @@ template <int LAYOUT, int KS, int NSS, int MAXM, bool STREAM, int RG, typename X
 __device__ __forceinline__ void linear_decode_block(
     const XT *__restrict__ x, const uint8_t *__restrict__ packed,
     const GammaMap &gm, int M, int64_t N, int64_t K, int64_t rb,
-    YT *__restrict__ y, int32_t *__restrict__ acc_out, const E &ep) {
+    OutPtr<YT, E> y, int32_t *__restrict__ acc_out, const E &ep) {
     using C = SkinnyCfg<LAYOUT>;
     constexpr int kThreads = 64 * KS;
     constexpr int kRoundUnits = KS * NSS * 4;
@@ -909,7 +909,7 @@ template <int LAYOUT, int KS, int NSS, int MAXM, bool STREAM, int RG, typename X
 __global__ __launch_bounds__(64 * KS) void linear_decode_epilogue_kernel(
     const XT *__restrict__ x, const uint8_t *__restrict__ packed,
     const GammaMap gm, int M, int64_t N, int64_t K, int64_t rb,
-    YT *__restrict__ y, const Epilogue<YT> ep) {
+    YT *y, const Epilogue<YT> ep) {
     linear_decode_block<LAYOUT, KS, NSS, MAXM, STREAM, RG, XT, YT>(x, packed, gm, M, N, K, rb, y,
                                                                    nullptr, ep);
 }

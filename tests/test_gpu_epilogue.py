@@ -284,3 +284,22 @@ def test_offsets_past_32_bits(bl):
     r = bl.bitlinear_epilogue_backward(res, z, "gelu", grad_bias=None)
     r2 = bl.bitlinear_epilogue_backward(res[rows], z[rows], "gelu", grad_bias=None)
     assert torch.equal(r.grad_z[rows], r2.grad_z)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 1003, 520), (1, 33000, 520), (2, 16390, 512), (4, 33000, 512),
+                                   (3, 12000, 4096), (3, 12001, 512), (4, 1001, 1003), (2, 5, 7)])
+@pytest.mark.parametrize("out", list(TYPES))
+def test_fused_residual_in_place(bl, M, N, K, out):
+    """residual == y in the fused products: one token and several, two and four row
+    groups, streamed tiles (12000 rows and more of 16-byte K), widths that four does not divide."""
+    print(f"[case] fused in place M={M} N={N} K={K} {out}", flush=True)
+    p = Problem(bl, M, N, K, seed=6)
+    bias, res = p.rand(N), p.rand(M, N, dtype=TYPES[out])
+    want = run(p, "x", bias=bias, act="silu", residual=res, residual_scale=0.5)
+    p.check(want, None, bias, "silu", res, 0.5)
+    y, guard = guarded((M, N), TYPES[out])
+    for _ in range(3):
+        y.copy_(res)
+        got = run(p, "x", bias=bias, act="silu", residual=y, residual_scale=0.5, y=y)
+        assert got is y and torch.equal(y, want)
+    guard.check("y", all_written=False)
