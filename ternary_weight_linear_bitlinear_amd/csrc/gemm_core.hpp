@@ -200,6 +200,7 @@ __device__ __forceinline__ int xcd_tile(int b, int ntiles) {
 // row's chunks one contiguous permutation for the reads.
 template <int BN>
 __device__ __forceinline__ int frag_slot(int row, int chunk) {
+    static_assert(BN % 128 == 0, "chunk ^ row, row < 32, stays within a row of BN / 4 chunks");
     return (row * (BN / 4) + (chunk ^ row)) * 16;
 }
 template <int BN>

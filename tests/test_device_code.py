@@ -50,3 +50,13 @@ def test_products_in_place_make_no_false_promise(tmp_path):
     assert sorted(unaliased_outputs(code, "12skinny_block")) == [4, 5]
     assert unaliased_outputs(code, "20linear_decode_kernel") == [4]
     assert unaliased_outputs(code, "13skinny_kernel") == [5]
+
+
+@pytest.mark.parametrize("BN,fits", [(64, False), (128, True), (256, True)])
+def test_staged_rows_hold_their_permutation(tmp_path, BN, fits):
+    """A staged row of BN sums has BN / 4 chunks, and its permutation chunk ^ row takes
+    rows up to 31: narrower rows than 128 would leave their memory, and do not compile."""
+    slots = {(r * (BN // 4) + (c ^ r)) for r in range(32) for c in range(BN // 4)}
+    assert (slots == set(range(32 * BN // 4))) is fits
+    rc, err, _ = compile_snippet(tmp_path, "gemm_core.hpp", f"template __device__ int frag_slot<{BN}>(int, int);")
+    assert (rc == 0) is fits, err
