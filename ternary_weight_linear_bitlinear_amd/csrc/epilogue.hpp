@@ -69,6 +69,28 @@ struct Epilogue {
 #pragma unroll
         for (int e = 0; e < C; ++e) b[e] = bias && n + e < N ? bias_at(n + e) : 0.f;
     }
+    // pieces of four bf16 or fp32 values, and of eight bf16, as loaded and as stored
+    __device__ __forceinline__ static void unpack(const uint2 &q, float (&v)[4]) {
+        const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            v[e] = __uint_as_float(w[e / 2] << 16);
+            v[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ static void unpack(const uint4 &q, float (&v)[8]) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            v[e] = __uint_as_float(w[e / 2] << 16);
+            v[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ static void unpack(const uint4 &q, float (&v)[4]) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+    }
     template <int C>
     __device__ __forceinline__ static void load(const YT *p, float (&v)[C]) {  // C * sizeof(YT) aligned
         if constexpr (sizeof(YT) == 4) {
@@ -77,15 +99,10 @@ struct Epilogue {
                 const float4 q = *reinterpret_cast<const float4 *>(p + e);
                 v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
             }
+        } else if constexpr (C == 8) {
+            unpack(*reinterpret_cast<const uint4 *>(p), v);
         } else {
-            uint32_t w[C / 2];
-            if constexpr (C == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(p);
-            else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(p);
-#pragma unroll
-            for (int e = 0; e < C; e += 2) {
-                v[e] = __uint_as_float(w[e / 2] << 16);
-                v[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
-            }
+            unpack(*reinterpret_cast<const uint2 *>(p), v);
         }
     }
     template <int C>
@@ -101,8 +118,8 @@ struct Epilogue {
                 const bf16x2 q = {(__bf16)v[e], (__bf16)v[e + 1]};
                 w[e / 2] = __builtin_bit_cast(uint32_t, q);
             }
-            if constexpr (C == 8) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(w);
-            else *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(w);
+            if constexpr (C == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
         }
     }
 

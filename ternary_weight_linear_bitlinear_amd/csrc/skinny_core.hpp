@@ -215,7 +215,8 @@ __device__ __forceinline__ void store_outputs(const GammaMap &gm,
 template <typename YT>
 struct EpilogueAhead {
     uint2 b0, b1;
-    uint32_t res[sizeof(YT)];  // four outputs
+    using Four = std::conditional_t<sizeof(YT) == 4, uint4, uint2>;
+    Four res;  // four outputs
     __device__ __forceinline__ void fetch(const Epilogue<YT> &ep, const void *valid, int64_t m,
                                           int64_t n, int64_t N) {
         const bool fast = N % 4 == 0;
@@ -226,10 +227,7 @@ struct EpilogueAhead {
         b1 = *reinterpret_cast<const uint2 *>(bp + off + (ep.bias && fast && !ep.bias_bf16 ? 8 : 0));
         const bool r = ep.residual && fast;
         const YT *rp = r ? ep.residual + (m * N + nc) : static_cast<const YT *>(valid);
-        if constexpr (sizeof(YT) == 4)
-            *reinterpret_cast<uint4 *>(res) = *reinterpret_cast<const uint4 *>(rp);
-        else
-            *reinterpret_cast<uint2 *>(res) = *reinterpret_cast<const uint2 *>(rp);
+        res = *reinterpret_cast<const Four *>(rp);
     }
     __device__ __forceinline__ void store(const GammaMap &gm, const float (&gs)[kMaxSegments],
                                           float scale, const v4i tot, int64_t m, int64_t n, int64_t N,
@@ -246,7 +244,7 @@ struct EpilogueAhead {
                 const uint32_t h = i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16;
                 b[i] = __uint_as_float(ep.bias_bf16 ? h : w[i]);
             }
-            Epilogue<YT>::load(reinterpret_cast<const YT *>(res), r);
+            Epilogue<YT>::unpack(res, r);
         } else {
             ep.load_bias(n, N, b);
             ep.load_residual(m * N + n, n, N, vec, r);

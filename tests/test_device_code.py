@@ -60,3 +60,13 @@ def test_staged_rows_hold_their_permutation(tmp_path, BN, fits):
     assert (slots == set(range(32 * BN // 4))) is fits
     rc, err, _ = compile_snippet(tmp_path, "gemm_core.hpp", f"template __device__ int frag_slot<{BN}>(int, int);")
     assert (rc == 0) is fits, err
+
+
+def test_fetched_pieces_keep_their_type(tmp_path):
+    """What the decode epilogue fetches ahead is held in the type that it is loaded
+    in and taken apart by value, not read back through pointers of other types."""
+    body = """
+        static_assert(std::is_same_v<decltype(EpilogueAhead<float>::res), uint4>);
+        static_assert(std::is_same_v<decltype(EpilogueAhead<uint16_t>::res), uint2>);"""
+    rc, err, _ = compile_snippet(tmp_path, "skinny_core.hpp", body)
+    assert rc == 0, err
