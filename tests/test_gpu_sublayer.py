@@ -203,3 +203,40 @@ def test_outputs_belong_to_the_given_stream(bl):
     torch.cuda.synchronize()
     for r in got:
         assert torch.equal(r.grad_z, want.grad_z) and torch.equal(r.grad_bias, want.grad_bias)
+
+
+@pytest.mark.parametrize("M,K,F,layout", [(16, 520, 1032, "2bit"), (3, 264, 520, "base3"), (200, 512, 1024, "1bit")])
+def test_sublayer_on_a_bf16_stream(bl, M, K, F, layout):
+    """The stream in bf16: the residual is h_out as stored. y is the rounded sum of
+    the down-projection and that residual, so against an unrounded h' it may be off by
+    h_out's half step and its own; and a run repeats itself bit for bit."""
+    s = Sublayer(bl, M, K, F, "2bit" if layout == "1bit" else layout, seed=M)
+    if layout == "1bit":
+        g = torch.Generator(device="cuda").manual_seed(M)
+        s.up, s.down = (bl.bitlinear_pack_weights(torch.randn(a, b, generator=g, device="cuda") * 0.05, layout, "binary")
+                        for a, b in ((F, K), (K, F)))
+    stream = s.h.to(BF16)
+    (pu, gu), (pd, gd) = s.up, s.down
+
+    def once():
+        a = bl.bitlinear_block_norm(stream, s.block, pre=s.pre, post=s.post, gate=s.gate, normed=False, quant=True)
+        u = bl.bitlinear_forward_epilogue(a.xq, a.scale, pu, gu, F, K, layout, bias=s.up_bias, act="relu2")
+        uq, us = bl.bitlinear_quant_acts(u)
+        y = bl.bitlinear_forward_epilogue(uq, us, pd, gd, K, F, layout, bias=s.down_bias, residual=a.h_out)
+        return a, u, uq, us, y
+
+    a, u, uq, us, y = once()
+    assert a.h_out.dtype == BF16 and y.dtype == BF16
+    d = lambda t: t.detach().cpu().double()  # noqa: E731
+    post = {"kind": "rms", "weight": d(s.post.weight), "bias": None, "eps": 1e-5}
+    args = (d(stream), d(s.block), None, post, d(s.gate), 1.0)
+    h64, th = ref.block64(*args)[0], ref.block_tols(*args)[0]
+    ref.close(a.h_out, h64, th, "h_out")
+    down = d(uq) * (d(us)[:, None] / 127) @ (codes64(bl, pd, K, F, layout) * d(gd)).t() + d(s.down_bias)
+    tol = ref.U * (8 * (down - d(s.down_bias)).abs() + 2 * d(s.down_bias).abs() + 2 * d(a.h_out).abs()
+                   + (down + d(a.h_out)).abs())
+    ref.close(y, down + d(a.h_out), tol, "y")
+    ref.close(y, down + h64, tol + th + ref.half_step(BF16) * (h64.abs() + th), "y against the unrounded stream")
+    for _ in range(3):
+        b, v, *_, w = once()
+        assert torch.equal(b.h_out, a.h_out) and torch.equal(v, u) and torch.equal(w, y)
