@@ -86,7 +86,6 @@ struct GemmCfg {
     // The extended epilogue stages INT32 fragment rows (32 x BN) in the same
     // memory: as many at a time as fit, one at least.
     static constexpr int kFragRow = 32 * BN * 4;
-    template <typename E>
     static constexpr int kEpiFrags = SMEM - LUT >= kFragRow ? (SMEM - LUT) / kFragRow : 1;
     template <typename E>
     static constexpr int kSmem = E::kActive && SMEM - LUT < kFragRow ? LUT + kFragRow : SMEM;
@@ -627,7 +626,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     const bool one = gm.nseg == 1;
     if constexpr (E::kActive) {
         static_assert(WM == 1, "a fragment row is staged by one row of waves");
-        constexpr int FP = C::template kEpiFrags<E>;  // fragment rows staged at a time
+        constexpr int FP = C::kEpiFrags;  // fragment rows staged at a time
         __shared__ float rowf[BM];
         stage_row_factors<BM, kThreads>(rowf, gm, gs[0], scale, m0, M);
         const RowEpilogue<BN, kThreads, YT, E> rows(ep, gm, gs, rowf, m0, n0, M, N, ldy, y);
@@ -1192,8 +1191,7 @@ hipError_t launch_gemm_tile(const int8_t *xq, const float *scale, const uint8_t 
     const int64_t ntiles = (int64_t)tm * tn;
     const int64_t blocks = (ntiles + kXcds - 1) / kXcds * kXcds;
     GemmArgs<YT> g{xq, scale, packed, gamma, M, N, K, rb, tm, tn, y, ldy, acc};
-    // (128 x 64 tiles keep row order: banded, they measured 2-4% slower)
-    g.band = BM == 128 && BN == 64 ? 1 : tile_band(tm, tn, (int64_t)BM * K, (int64_t)BN * rb);
+    g.band = tile_band(tm, tn, (int64_t)BM * K, (int64_t)BN * rb);
     auto launch = [&](auto kern, LdsFlag *flag) {
         hipError_t e = allow_dynamic_lds(kern, C::template kSmem<E>, flag);
         if (e != hipSuccess) return e;
