@@ -223,14 +223,18 @@ def run(s):
 def run_own(s):
     from ternary_weight_linear_bitlinear_amd import bitlinear as bl
     if s["op"] == "layer":
-        r = bl.bitlinear_block_norm(s["stream"], s["block_out"], pre=own_norm(bl, s["pre"]), post=own_norm(bl, s["post"]),
-                                    gate=s["gate"], normed=False, quant=True, **s["norm_new"])
+        # y adds the unrounded h': the stream is widened for the sublayer and rounded where it leaves it
+        # (h_out, the residual and y have the stream's type, so a bf16 residual would be rounded once more)
+        new = s["norm_new"]
+        r = bl.bitlinear_block_norm(s["stream"].float(), s["block_out"], pre=own_norm(bl, s["pre"]),
+                                    post=own_norm(bl, s["post"]), gate=s["gate"], normed=False, quant=True,
+                                    xq=new["xq"], scale=new["scale"])
         up, down = s["up"], s["down"]
         u = bl.bitlinear_forward_epilogue(r.xq, r.scale, up["packed"], up["gammas"], up["N"], up["K"], up["layout"],
                                           bias=s["up_bias"], act="relu2", y=s["new"]["u"])
         y = bl.linear_epilogue(u, down["packed"], down["gammas"], down["N"], down["layout"], bias=s["down_bias"],
-                               residual=r.h_out, y=s["new"]["y"])
-        return {"h_out": r.h_out, "y": y}
+                               residual=r.h_out)
+        return {"h_out": new["h_out"].copy_(r.h_out), "y": s["new"]["y"].copy_(y)}
     if s["op"] == "norm":
         norms = {"pre": own_norm(bl, s["pre"]), "post": own_norm(bl, s["post"])}
         if s["back"]:
