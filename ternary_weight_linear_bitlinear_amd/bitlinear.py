@@ -541,7 +541,8 @@ def bitlinear_forward_epilogue(xq: torch.Tensor, scale: torch.Tensor, packed: to
     bitlinear_forward (bitlinear_forward_segmented) + bias.
 
     seg_rows: N, or the row counts of stacked matrices (gammas[s] each).
-    residual may be y itself. out_dtype defaults to y's, then residual's type,
+    residual may be y itself; it is added as stored, so a bf16 residual is rounded
+    before the sum. out_dtype defaults to y's, then residual's type,
     then fp32; y, z and residual share it. Returns y, or (y, z) when z is
     requested."""
     if stream is not None:
@@ -629,7 +630,7 @@ def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, ac
     """Gradients of y = act(z) + residual_scale * residual, z = product + bias:
     grad_z [M, N] (out_dtype, grad_y's type by default), grad_bias [N] fp32,
     grad_residual [M, N] of grad_y's type. Each is a buffer, True (allocate) or
-    None (leave out). z may be None for act "none"."""
+    None (leave out); none may overlap grad_y or z. z may be None for act "none"."""
     if stream is not None:
         with _on("bitlinear_epilogue_backward", stream, grad_y):
             return bitlinear_epilogue_backward(grad_y, z, act, residual_scale, out_dtype, grad_z, grad_bias,
@@ -813,7 +814,8 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
     them; grad_h_out: the gradient of h_out from its other uses (None: zero);
     grad_n: the gradient of n (None without pre), or of the quantised input
     (straight-through). Parameter gradients are fp32 [K] (a gate per token: [M, K]
-    of block's type); params=False leaves out those that no buffer is given for."""
+    of block's type); params=False leaves out those that no buffer is given for. No
+    output may overlap an input (grad_h is not grad_h_out)."""
     if stream is not None:
         with _on("bitlinear_block_norm_backward", stream, h_out):
             return bitlinear_block_norm_backward(grad_h_out, grad_n, h_out, block, stats, pre, post, gate,

@@ -1241,9 +1241,11 @@ hipError_t launch_gemm_cols(const int8_t *xq, const float *scale, const uint8_t 
     const int64_t ktiles = (units + 1) / 2;
     const bool long_k = ktiles >= 64;
     // k-tiles from which two groups splitting them pay off on few tiles (see
-    // below); rows of K % 16 != 0 bytes load piecewise, take longer per
-    // k-tile and gain from 16 on (200 x 2000 x 3000: 2-bit 23.2 -> 19.5 us,
-    // base-3 39.7 -> 34.5 us)
+    // below); rows of K % 16 != 0 bytes load in unaligned pieces, take longer per
+    // k-tile and gain from 16 on. 64 to 512 tokens, split against unsplit, over nine
+    // sizes each: 2-bit and 1-bit 5 to 10% faster at 17 k-tiles, 17 to 23% at 28
+    // (200 x 2000 x 3000: 13.9 -> 11.2 us), base-3 from 1% slower to 6% faster at 17,
+    // 5 to 10% at 26 (200 x 2000 x 4100: 23.9 -> 21.5 us); more with the extended epilogue.
     const int64_t split_kt = K % 16 != 0 ? 16 : 32;
 #define BL_GEMM_TILE(...)                                                                    \
     return launch_gemm_tile<LAYOUT, __VA_ARGS__>(xq, scale, packed, gamma, M, N, K, y, ldy, acc, \

@@ -46,8 +46,11 @@ __device__ __forceinline__ float block_max(float v) {
 // ---------------------------------------------------------------------------
 // Forward, rows that holds_row() accepts: one workgroup per row, the row held in registers
 // from its one read to its one write. Memory-bound: 2048 x 4096 (fp32
-// stream, bf16 block, 101 MB) 19.5 us, 5.2 TB/s, against 5.1 TB/s for a 1 GiB copy; 8192
-// rows 78 us. One row of 4096 takes 2.9 us, which is latency.
+// stream, bf16 block, 101 MB) 24 to 26 us, 4 TB/s, against 5.1 TB/s for a 1 GiB copy (19 us
+// where the outputs stay in the caches); 8192 rows 76 us, 5.3 TB/s. Codes in place of
+// values 23.6 us (92 MB), values, codes and statistics 28.7 us (109 MB). 2048 x 11008
+// 60 us, 2048 x 16384 84 us, 1024 x 32768 99 us (four chunks: 4.1 TB/s). One row of 4096
+// takes 2.9 us, which is latency.
 //
 // Thread t owns J chunks of eight consecutive elements (chunks t, t + T, ...;
 // row_share.hpp). Every load of the row is issued before the first reduction. A
@@ -57,8 +60,18 @@ constexpr int kMaxWaves = 16;
 constexpr int64_t kRegElems = 8 * 64 * kMaxWaves;  // of a row, for each chunk per thread
 // Chunks per thread: the fewest threads that hold the row wait least on one
 // another, the most finish a single row soonest. From two rows per compute unit on
-// rows of 2048 elements and more take two chunks (8192 x 4096 84.3 -> 78.4 us, 2048
-// x 8192 49.9 -> 39.7 us; 4096 x 1024 12.1 -> 12.6 us, so shorter rows keep one).
+// rows of 2048 elements and more take two chunks. Their time against one chunk's (RMS, bf16
+// block, with an fp32 and with a bf16 stream, more data than the caches hold):
+//   width     333 rows   512        1024       2048       8192
+//   2048     +15 +17%   +14 +17%    +5  +3%     0  +1%    +5  +1%
+//   4096      +3  +5%    +5  +6%    -3  -2%    +5  -2%     0  -8%
+//   5001      +2  -3%    +6  -2%   -14 -31%    -4 -21%   -11 -26%
+//   6144       0  -2%    +6  +3%    +1  -8%    +2  -4%    -6 -13%
+//   8192     -10 -17%   -11  -7%   -12 -16%   -12 -23%   -17 -29%
+// (8192 x 8192 bf16 144.5 -> 101.9 us, 512 x 2048 4.6 -> 5.4 us.) The narrow end of the
+// rule costs up to 0.8 us a call; rows of 8192 would gain from 257 rows on.
+// Rows of more than 16384 elements take four chunks, which with an fp32 block
+// spill 8 to 53 registers (1024 x 32768 118 us, 4.5 TB/s).
 constexpr int64_t kManyRows = 512;
 inline bool holds_row(int64_t K) { return K >= 8 && K <= 4 * kRegElems; }
 
@@ -306,6 +319,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 // Other rows: one row per workgroup, any K: each statistic is a pass over the row (which
 // stays in the caches), the last pass writes. Every element is read and written
 // by one thread, and nothing is written before the last pass, so h_out may be h.
+// 512 x 40000 387 us, 0.6 TB/s; one row of 40000 171 us: single elements by 256 threads,
+// a few waves a row. Usual hidden widths lie between these rows' (under 8, over 32768).
 template <typename HT, typename XT, typename PT>
 __global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNormArgs a,
                                                                    int64_t m0) {
@@ -387,6 +402,10 @@ __global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNo
 // and the lost overlap cost more than the extra waves give (8192 x 4096: 128 runs
 // 179 us, 256 138 us, 512 143 us, 1024 151 us; 4096 x 4096 fp32 stream and grad_n,
 // 335 MB, 70 us, 4.8 TB/s, and 5 us for the sums).
+// Rows of two chunks spill: up to 65 registers without biases, 26 to 185 with them (four
+// column sums of two chunks are 64 registers beside two rows). 2048 x 8192, the
+// sums included: RMS 90.6 us (3.7 TB/s), LayerNorm with biases 124 us (2.7), fp32
+// throughout 119 and 175 us, bf16 throughout 56 and 75 us.
 constexpr int64_t kChunkRows = 512;
 constexpr int kGradThreads = 512;  // at most: two waves of 256 registers per SIMD
 inline bool grad_holds_row(int64_t K) { return K >= 8 && K <= 2 * 8 * kGradThreads; }
@@ -612,7 +631,9 @@ __global__ __launch_bounds__(32 * kSumRows) void block_norm_grad_sums_kernel(
 }
 
 // Other rows: a workgroup per row with a pass per statistic, then the columns
-// in a kernel of their own that forms d again.
+// in a kernel of their own that forms d again. Single elements, and every input
+// walked several times: 2048 x 11008 453 us, 2048 x 16384 686 us (1 TB/s of what
+// must move).
 template <typename HT, typename XT, typename NT, typename PT>
 struct GradRow {
     const BlockNormGradArgs &a;
