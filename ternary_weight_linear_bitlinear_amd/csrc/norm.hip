@@ -320,7 +320,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(const BlockN
 // stays in the caches), the last pass writes. Every element is read and written
 // by one thread, and nothing is written before the last pass, so h_out may be h.
 // 512 x 40000 387 us, 0.6 TB/s; one row of 40000 171 us: single elements by 256 threads,
-// a few waves a row. Usual hidden widths lie between these rows' (under 8, over 32768).
+// four waves a row. Usual hidden widths lie between these rows' (under 8, over 32768).
 template <typename HT, typename XT, typename PT>
 __global__ __launch_bounds__(kThreads) void block_norm_rows_kernel(const BlockNormArgs a,
                                                                    int64_t m0) {
