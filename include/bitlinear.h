@@ -328,6 +328,119 @@ bl_status bitlinear_epilogue_backward(const void *grad_y, int gy_dtype, const vo
                                       int gz_dtype, float *grad_bias, void *grad_residual,
                                       void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Gated feed-forward products -------------------------------------------
+ *
+ * The two up-projections of a gated feed-forward block, its activation and their
+ * product in one launch. The matrices are a stack of two (as for
+ * bitlinear_forward_segmented, nseg = 2) of F rows each: rows 0 .. F - 1 the gate
+ * with gammas[0], rows F .. 2F - 1 the other with gammas[1].
+ *   z[m, h F + f] = gammas[h] * scale[m] / 127 * acc[m, h F + f] + bias[h F + f]
+ *   y[m, f] = act(z[m, f]) * z[m, F + f]
+ * acc is the exact INT32 sum; everything after it is fp32, rounded once to y's type. */
+
+/* bitlinear_forward_gated:
+ *   F        rows of each matrix, 1 <= F < 2^30.
+ *   bias     [2F] bias_dtype, or NULL.
+ *   z        optional out: [M, 2F] of y's type, the pre-activations, or NULL.
+ *   codes, code_scale  optional out (both or neither): the pre-activations in fp32
+ *            as the 8-bit checkpoint of bitlinear_checkpoint over [2M, F], that is
+ *            of z seen as rows 2m (gate) and 2m + 1: [2M, F] int8 and [2M,
+ *            bitlinear_checkpoint_groups(F)] float. Asked for, the product runs on
+ *            the tiled kernels at any M.
+ *   y        out: [M, F] y_dtype.
+ * Other arguments, limits and errors as for bitlinear_forward_epilogue. No output
+ * may overlap another argument. */
+bl_status bitlinear_forward_gated(const int8_t *xq, const float *scale, const uint8_t *packed,
+                                  int layout, const float *gammas, int64_t F, int64_t M, int64_t K,
+                                  const void *bias, int bias_dtype, int act, void *z,
+                                  int8_t *codes, float *code_scale, void *y, int y_dtype,
+                                  void *stream);
+
+/* bitlinear_linear_gated: the same from unquantised x, fused into one launch as
+ * bitlinear_linear (1 <= M <= 4, else BL_ERR_UNSUPPORTED), without a checkpoint. */
+bl_status bitlinear_linear_gated(const void *x, int x_dtype, const uint8_t *packed, int layout,
+                                 const float *gammas, int64_t F, int64_t M, int64_t K,
+                                 const void *bias, int bias_dtype, int act, void *z, void *y,
+                                 int y_dtype, void *stream);
+
+/* Device workspace (bytes) of bitlinear_gated_backward; 0 for an empty or refused
+ * shape. */
+size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F);
+
+/* Backward of the gated epilogue:
+ *   grad_z[m, f]     = grad_y[m, f] * z[m, F + f] * act'(z[m, f])
+ *   grad_z[m, F + f] = grad_y[m, f] * act(z[m, f])
+ *   grad_bias[n]     = sum_m grad_z[m, n]
+ * grad_z is what bitlinear_backward_input_segmented and the weight gradients take as
+ * their grad_y.
+ *   grad_y   [M, F] gy_dtype.
+ *   z        [M, 2F] z_dtype, or NULL: then codes [2M, F] and code_scale [2M,
+ *            bitlinear_checkpoint_groups(F)], the checkpoint that the forward pass
+ *            left (exactly one of z and the pair is given).
+ *   grad_z   out [M, 2F] gz_dtype, or NULL.
+ *   grad_bias out [2F] fp32, or NULL: fp32 sums of the unrounded grad_z over at most
+ *            512 tokens at a time, added in fp64 in a fixed order. Needs the workspace.
+ * relu's slope at 0 is 0. At least one output is required; outputs may not overlap
+ * inputs. M at most 2^23, F at most 2^23. M = 0 writes zeros to grad_bias. */
+bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void *z, int z_dtype,
+                                   const int8_t *codes, const float *code_scale, int act,
+                                   int64_t M, int64_t F, void *grad_z, int gz_dtype,
+                                   float *grad_bias, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* ---- Activations kept in 8 bits ---------------------------------------------
+ *
+ * What a training step holds between its forward and its backward pass, at 1.06
+ * bytes an element: the quantiser of bitlinear_quant_acts with a scale for each 64
+ * columns of a row (the last group of a row may be shorter),
+ *   s = max(max|x|, 1e-6) over the group, q = clamp(round(x / s * 127), -127, 127),
+ * and a kept value stands for q * (s / 127), within s / 254 of x. */
+
+/* Scales of a row of K columns: ceil(K / 64); 0 for K < 1. Host-only, pure. */
+int64_t bitlinear_checkpoint_groups(int64_t K);
+
+/* bitlinear_checkpoint: x [M, K] x_dtype into codes [M, K] int8 and scale [M,
+ * bitlinear_checkpoint_groups(K)] float. M, K at most 2^24; M = 0 is a no-op. */
+bl_status bitlinear_checkpoint(const void *x, int x_dtype, int64_t M, int64_t K, int8_t *codes,
+                               float *scale, void *stream);
+
+/* bitlinear_checkpoint_restore: the kept values as y [M, K] y_dtype (fp32 products,
+ * rounded once). */
+bl_status bitlinear_checkpoint_restore(const int8_t *codes, const float *scale, int64_t M, int64_t K,
+                                       void *y, int y_dtype, void *stream);
+
+/* bitlinear_backward_weight_codes: the weight gradient from the codes that the
+ * forward product had, so that x itself need not be kept ([b158] §5.3 takes the
+ * gradient with the dequantised x):
+ *   grad_w[n, k] = sum_m (grad_y[m, n] * (scale[m] / 127)) * xq[m, k]
+ *   grad_y   [M, N] gy_dtype; xq [M, K], scale [M]: from bitlinear_quant_acts.
+ *   grad_w   out [N, K] gw_dtype. BL_F32: the factor in parentheses is rounded once
+ *            to fp32 and enters as three exact bf16 pieces (for magnitudes >= 2^-110,
+ *            as in bitlinear_backward_input), so products are exact and sums fp32;
+ *            three times the matrix-core work of bf16. BL_BF16: two pieces (the
+ *            factor to within 2^-15 of its magnitude), fp32 sums, rounded once.
+ * Any N and K (multiples of 8 and 16 load faster). Dimensions above 2^24 return
+ * BL_ERR_INVALID_ARG. N = 0 is a no-op; M = 0 writes zeros. */
+bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
+                                          const float *scale, int64_t M, int64_t N, int64_t K,
+                                          void *grad_w, int gw_dtype, void *stream);
+
+/* bitlinear_backward_input_segmented: the gradient of the input that a stack shares,
+ *   grad_x[m, k] = sum_s gammas[s] * sum_{n in segment s} grad_y[m, n] * c[n, k]
+ *   grad_y   [M, N] gy_dtype, N = sum(seg_rows); fp32 values are split exactly as in
+ *            bitlinear_backward_input.
+ *   packed, layout, gammas, seg_rows, nseg: as in bitlinear_forward_segmented (one
+ *            segment: a plain matrix).
+ *   grad_x   out [M, K] gx_dtype (fp32 sums, rounded once). The sums are rescaled by
+ *            the ratio of two segments' gammas where one ends, one fp32 rounding each.
+ * Any N and K (row counts that are multiples of 8 load faster). Dimensions above 2^24
+ * return BL_ERR_INVALID_ARG. M = 0 is a no-op. */
+bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
+                                             const uint8_t *packed, int layout,
+                                             const float *gammas, const int64_t *seg_rows, int nseg,
+                                             int64_t M, int64_t K, void *grad_x, int gx_dtype,
+                                             void *stream);
+
 /* ---- Norms before and after a block ----------------------------------------
  *
  * What stands between two blocks of a transformer layer, in one pass over the

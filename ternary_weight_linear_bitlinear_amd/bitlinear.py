@@ -14,6 +14,14 @@ Around the product: ``bitlinear_forward_epilogue`` / ``bitlinear_linear_epilogue
 (``linear_epilogue`` picks one) add bias, activation and residual,
 ``bitlinear_block_norm`` takes the norms before and after a block with the gate
 and the residual stream between them; each has its backward call.
+
+A gated feed-forward block: ``bitlinear_forward_gated`` / ``bitlinear_linear_gated``
+(``linear_gated`` picks one) run both up-projections, the activation and their
+product, ``bitlinear_gated_backward`` goes back. A training step keeps 8-bit codes
+between the two: ``bitlinear_checkpoint`` / ``bitlinear_checkpoint_restore`` (the
+gated calls write and read them directly), ``bitlinear_backward_weight_codes`` takes
+the weight gradient from the product's own codes, and
+``bitlinear_backward_input_segmented`` the gradient of an input that a stack shares.
 """
 from __future__ import annotations
 
@@ -118,6 +126,28 @@ _lib.bitlinear_block_norm_backward.restype = _int
 _lib.bitlinear_block_norm_backward.argtypes = [_p, _p, _int, _p, _int, _p, _int, _p, _f32, _p, _int,
                                                _int, _p, _p, _int, _p, _int, _i64, _i64, _p, _p,
                                                _p, _p, _p, _p, _p, _p, _sz, _p]
+_lib.bitlinear_forward_gated.restype = _int
+_lib.bitlinear_forward_gated.argtypes = [_p, _p, _p, _int, _p, _i64, _i64, _i64, _p, _int, _int,
+                                         _p, _p, _p, _p, _int, _p]
+_lib.bitlinear_linear_gated.restype = _int
+_lib.bitlinear_linear_gated.argtypes = [_p, _int, _p, _int, _p, _i64, _i64, _i64, _p, _int, _int,
+                                        _p, _p, _int, _p]
+_lib.bitlinear_gated_backward_workspace_bytes.restype = _sz
+_lib.bitlinear_gated_backward_workspace_bytes.argtypes = [_i64, _i64]
+_lib.bitlinear_gated_backward.restype = _int
+_lib.bitlinear_gated_backward.argtypes = [_p, _int, _p, _int, _p, _p, _int, _i64, _i64, _p, _int,
+                                          _p, _p, _sz, _p]
+_lib.bitlinear_checkpoint_groups.restype = _i64
+_lib.bitlinear_checkpoint_groups.argtypes = [_i64]
+_lib.bitlinear_checkpoint.restype = _int
+_lib.bitlinear_checkpoint.argtypes = [_p, _int, _i64, _i64, _p, _p, _p]
+_lib.bitlinear_checkpoint_restore.restype = _int
+_lib.bitlinear_checkpoint_restore.argtypes = [_p, _p, _i64, _i64, _p, _int, _p]
+_lib.bitlinear_backward_weight_codes.restype = _int
+_lib.bitlinear_backward_weight_codes.argtypes = [_p, _int, _p, _p, _i64, _i64, _i64, _p, _int, _p]
+_lib.bitlinear_backward_input_segmented.restype = _int
+_lib.bitlinear_backward_input_segmented.argtypes = [_p, _int, _p, _int, _p, _p, _int, _i64, _i64,
+                                                    _p, _int, _p]
 _lib.bitlinear_forward_plan.restype = _int
 _lib.bitlinear_forward_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, ctypes.c_char_p, _sz]
 _lib.bitlinear_status_string.restype = ctypes.c_char_p
@@ -133,7 +163,11 @@ EXPORTED = ["bitlinear_packed_row_bytes", "bitlinear_pack_workspace_bytes",
             "bitlinear_forward_epilogue", "bitlinear_linear_epilogue",
             "bitlinear_epilogue_backward_workspace_bytes", "bitlinear_epilogue_backward",
             "bitlinear_block_norm", "bitlinear_block_norm_backward_workspace_bytes",
-            "bitlinear_block_norm_backward", "bitlinear_forward_plan", "bitlinear_status_string",
+            "bitlinear_block_norm_backward", "bitlinear_forward_gated", "bitlinear_linear_gated",
+            "bitlinear_gated_backward_workspace_bytes", "bitlinear_gated_backward",
+            "bitlinear_checkpoint_groups", "bitlinear_checkpoint", "bitlinear_checkpoint_restore",
+            "bitlinear_backward_weight_codes", "bitlinear_backward_input_segmented",
+            "bitlinear_forward_plan", "bitlinear_status_string",
             "bitlinear_version",
             "bitlinear_source_hash"]
 FUSED_MAX_M = 4
@@ -865,3 +899,267 @@ def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch
     _run(where, dev, _lib.bitlinear_block_norm_backward, args)
     return BlockNormGrads(grad_h, grad_block, grad_gate, grad_post_weight, grad_post_bias,
                           grad_pre_weight, grad_pre_bias)
+
+
+# ---- gated feed-forward products and activations kept in 8 bits --------------
+class Checkpoint(NamedTuple):
+    """A tensor [M, K] in 8 bits: codes [M, K] int8 and a scale for each 64 columns of
+    a row, [M, ceil(K / 64)] fp32. A value is code * (scale / 127)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+
+class GatedProduct(NamedTuple):
+    y: torch.Tensor
+    z: torch.Tensor | None
+    kept: Checkpoint | None
+
+
+class GatedGrads(NamedTuple):
+    grad_z: torch.Tensor | None
+    grad_bias: torch.Tensor | None
+
+
+def bitlinear_checkpoint_groups(K: int) -> int:
+    """Scales of a kept row of K columns."""
+    return -(-K // 64) if K > 0 else 0
+
+
+def _kept(where, kept, M, K, dev, t):
+    """A checkpoint of [M, K] and its addresses: the caller's (checked), or a new one
+    beside t where `kept` is True."""
+    shape = (M, bitlinear_checkpoint_groups(K))
+    if kept is True:
+        kept = Checkpoint(torch.empty(M, K, dtype=torch.int8, device=t.device),
+                          torch.empty(shape, dtype=_f32, device=t.device))
+        return kept, kept.codes.data_ptr(), kept.scale.data_ptr()
+    codes, scale = kept
+    return kept, _addr(where, "kept.codes", codes, (M, K), torch.int8, dev), \
+        _addr(where, "kept.scale", scale, shape, _f32, dev)
+
+
+def _code(dtype) -> int:
+    return BL_F32 if dtype is _f32 else BL_BF16
+
+
+def _out_dtype(where, out_dtype, given):
+    """The type of an output: as asked for, or that of the caller's buffer, or fp32."""
+    dtype = out_dtype or (given.dtype if given is not None else _f32)
+    if dtype is not _f32 and dtype is not _bf16:
+        _refuse(where, f"out_dtype is {dtype}")
+    return dtype
+
+
+def _gated(where, call, lead, M, K, dev, packed, gammas, F, layout, bias, act, out_dtype, y, z, kept, beside):
+    lay = _one_of(where, "layout", layout, LAYOUTS)
+    F = operator.index(F)
+    out_dtype = _out_dtype(where, out_dtype, y)
+    if y is None:
+        y = torch.empty(M, F, dtype=out_dtype, device=packed.device)
+    if z is True:
+        z = torch.empty(M, 2 * F, dtype=out_dtype, device=packed.device)
+    elif z is False:
+        z = None
+    if kept is False:
+        kept = None
+    keep = ()
+    if beside:  # the call that can leave a checkpoint
+        keep = (None, None)
+        if kept is not None:
+            kept, *keep = _kept(where, kept, 2 * M, F, dev, packed)
+    elif kept is not None:
+        _refuse(where, "the fused call leaves no checkpoint")
+    if gammas.dtype is not _f32 or gammas.numel() < 2 or gammas.get_device() != dev or not gammas.is_contiguous():
+        _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for 2 matrices, "
+                       "or is not contiguous")
+    args = (*lead, _addr(where, "packed", packed, (2 * F, _row_bytes(K, lay)), torch.uint8, dev), lay,
+            gammas.data_ptr(), F, M, K,
+            None if bias is None else _addr(where, "bias", bias, (2 * F,), _float(where, "bias", bias), dev),
+            BL_F32 if bias is None else _DTYPES[bias.dtype], _one_of(where, "act", act, ACTS),
+            None if z is None else _addr(where, "z", z, (M, 2 * F), out_dtype, dev), *keep,
+            _addr(where, "y", y, (M, F), out_dtype, dev), _code(out_dtype))
+    _run(where, dev, call, args)
+    return GatedProduct(y, z, kept)
+
+
+def bitlinear_forward_gated(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tensor,
+                            gammas: torch.Tensor, F: int, K: int, layout="2bit", bias=None, act="silu",
+                            out_dtype=None, y: torch.Tensor | None = None,
+                            z: torch.Tensor | bool | None = None,
+                            kept: Checkpoint | bool | None = None, stream=None) -> GatedProduct:
+    """y [M, F] = act(z[:, :F]) * z[:, F:] with z = the product of a stack of two
+    matrices of F rows (gate, then the other; gammas[0], gammas[1]) + bias [2F].
+
+    z (a buffer or True): also the pre-activations [M, 2F], of y's type. kept (a
+    Checkpoint or True): them in 8 bits for bitlinear_gated_backward, as
+    bitlinear_checkpoint gives for z in fp32 seen as [2M, F]. out_dtype defaults to
+    y's type, then fp32. No output may overlap another argument."""
+    if stream is not None:
+        with _on("bitlinear_forward_gated", stream, xq):
+            return bitlinear_forward_gated(xq, scale, packed, gammas, F, K, layout, bias, act, out_dtype, y, z, kept)
+    where = "bitlinear_forward_gated"
+    if xq.dim() != 2:
+        _refuse(where, f"xq has shape {tuple(xq.shape)}")
+    M, dev = xq.shape[0], xq.get_device()
+    lead = (_addr(where, "xq", xq, (M, K), torch.int8, dev), _addr(where, "scale", scale, (M,), _f32, dev))
+    return _gated(where, _lib.bitlinear_forward_gated, lead, M, xq.shape[1], dev, packed, gammas, F, layout, bias,
+                  act, out_dtype, y, z, kept, True)
+
+
+def bitlinear_linear_gated(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, F: int,
+                           layout="2bit", bias=None, act="silu", out_dtype=None,
+                           y: torch.Tensor | None = None, z: torch.Tensor | bool | None = None,
+                           stream=None) -> GatedProduct:
+    """bitlinear_forward_gated fused with the quantisation of x, M <= 4 tokens, without
+    a checkpoint."""
+    if stream is not None:
+        with _on("bitlinear_linear_gated", stream, x):
+            return bitlinear_linear_gated(x, packed, gammas, F, layout, bias, act, out_dtype, y, z)
+    where = "bitlinear_linear_gated"
+    (M, K), dtype, dev, x_at = _lead(where, "x", x)
+    return _gated(where, _lib.bitlinear_linear_gated, (x_at, _code(dtype)), M, K, dev, packed, gammas, F, layout,
+                  bias, act, out_dtype, y, z, None, False)
+
+
+def linear_gated(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, F: int, layout="2bit",
+                 bias=None, act="silu", out_dtype=None, y: torch.Tensor | None = None,
+                 z: torch.Tensor | bool | None = None, kept: Checkpoint | bool | None = None,
+                 stream=None) -> GatedProduct:
+    """``linear`` for a gated pair of matrices: one fused launch for M <= 4 without a
+    checkpoint, otherwise quantise then multiply."""
+    if stream is not None:
+        with _on("linear_gated", stream, x):
+            return linear_gated(x, packed, gammas, F, layout, bias, act, out_dtype, y, z, kept)
+    if x.dim() != 2 or (x.shape[0] <= FUSED_MAX_M and (kept is None or kept is False)):
+        return bitlinear_linear_gated(x, packed, gammas, F, layout, bias, act, out_dtype, y, z)
+    where = "linear_gated"
+    (M, K), dtype, dev, x_at = _lead(where, "x", x)
+    xq = torch.empty(M, K, dtype=torch.int8, device=x.device)
+    scale = torch.empty(M, dtype=_f32, device=x.device)
+    _run(where, dev, _lib.bitlinear_quant_acts, (x_at, _code(dtype), M, K, xq.data_ptr(), scale.data_ptr()))
+    return bitlinear_forward_gated(xq, scale, packed, gammas, F, K, layout, bias, act, out_dtype, y, z, kept)
+
+
+@functools.lru_cache(maxsize=1024)
+def bitlinear_gated_backward_workspace_bytes(M: int, F: int) -> int:
+    return int(_lib.bitlinear_gated_backward_workspace_bytes(M, F))
+
+
+def bitlinear_gated_backward(grad_y: torch.Tensor, z: torch.Tensor | Checkpoint, act="silu",
+                             out_dtype=None, grad_z: torch.Tensor | bool | None = True,
+                             grad_bias: torch.Tensor | bool | None = True,
+                             workspace: torch.Tensor | None = None, stream=None) -> GatedGrads:
+    """Gradients of y = act(z[:, :F]) * z[:, F:] for grad_y [M, F]: grad_z [M, 2F]
+    (out_dtype, grad_y's type by default) and its column sums grad_bias [2F] fp32.
+    z: the pre-activations [M, 2F], or the Checkpoint that the forward call left. Each
+    output is a buffer, True (allocate) or None (leave out); none may overlap an input."""
+    if stream is not None:
+        with _on("bitlinear_gated_backward", stream, grad_y):
+            return bitlinear_gated_backward(grad_y, z, act, out_dtype, grad_z, grad_bias, workspace)
+    where = "bitlinear_gated_backward"
+    (M, F), dtype, dev, gy_at = _lead(where, "grad_y", grad_y)
+    own = grad_z is not None and grad_z is not True and grad_z is not False
+    if out_dtype is None:
+        out_dtype = grad_z.dtype if own else dtype
+    out_dtype = _out_dtype(where, out_dtype, None)
+    if not own:
+        grad_z = torch.empty(M, 2 * F, dtype=out_dtype, device=grad_y.device) if grad_z else None
+    if grad_bias is True:
+        grad_bias = torch.empty(2 * F, dtype=_f32, device=grad_y.device)
+    elif grad_bias is False:
+        grad_bias = None
+    if isinstance(z, tuple):
+        _, codes, code_scale = _kept(where, z, 2 * M, F, dev, grad_y)
+        z_args = (None, BL_F32, codes, code_scale)
+    else:
+        z_args = (_addr(where, "z", z, (M, 2 * F), _float(where, "z", z), dev), _DTYPES[z.dtype], None, None)
+    need = bitlinear_gated_backward_workspace_bytes(M, F) if grad_bias is not None else 0
+    hold, ws, ws_bytes = (None, None, 0) if need == 0 else _workspace(where, workspace, need, grad_y)
+    args = (gy_at, _code(dtype), *z_args, _one_of(where, "act", act, ACTS), M, F,
+            None if grad_z is None else _addr(where, "grad_z", grad_z, (M, 2 * F), out_dtype, dev), _code(out_dtype),
+            None if grad_bias is None else _addr(where, "grad_bias", grad_bias, (2 * F,), _f32, dev), ws, ws_bytes)
+    _run(where, dev, _lib.bitlinear_gated_backward, args)
+    return GatedGrads(grad_z, grad_bias)
+
+
+def bitlinear_checkpoint(x: torch.Tensor, kept: Checkpoint | None = None, stream=None) -> Checkpoint:
+    """x [M, K] in 8 bits, a scale for each 64 columns of a row."""
+    if stream is not None:
+        with _on("bitlinear_checkpoint", stream, x):
+            return bitlinear_checkpoint(x, kept)
+    where = "bitlinear_checkpoint"
+    (M, K), dtype, dev, x_at = _lead(where, "x", x)
+    kept, codes, scale = _kept(where, True if kept is None else kept, M, K, dev, x)
+    _run(where, dev, _lib.bitlinear_checkpoint, (x_at, _code(dtype), M, K, codes, scale))
+    return kept
+
+
+def bitlinear_checkpoint_restore(kept: Checkpoint, out_dtype=None, y: torch.Tensor | None = None,
+                                 stream=None) -> torch.Tensor:
+    """The kept values as a tensor [M, K] (out_dtype: y's type by default, then fp32)."""
+    codes = kept[0]
+    if stream is not None:
+        with _on("bitlinear_checkpoint_restore", stream, codes):
+            return bitlinear_checkpoint_restore(kept, out_dtype, y)
+    where = "bitlinear_checkpoint_restore"
+    if codes.dim() != 2:
+        _refuse(where, f"kept.codes has shape {tuple(codes.shape)}")
+    (M, K), dev = codes.shape, codes.get_device()
+    _, codes_at, scale_at = _kept(where, kept, M, K, dev, codes)
+    out_dtype = _out_dtype(where, out_dtype, y)
+    if y is None:
+        y = torch.empty(M, K, dtype=out_dtype, device=codes.device)
+    _run(where, dev, _lib.bitlinear_checkpoint_restore,
+         (codes_at, scale_at, M, K, _addr(where, "y", y, (M, K), out_dtype, dev), _code(out_dtype)))
+    return y
+
+
+def bitlinear_backward_weight_codes(grad_y: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,
+                                    out_dtype=None, grad_w: torch.Tensor | None = None,
+                                    stream=None) -> torch.Tensor:
+    """grad_w [N, K] = sum_m grad_y[m, n] * (scale[m] / 127) * xq[m, k], from the codes
+    that the forward product had (out_dtype: grad_w's type by default, then fp32)."""
+    if stream is not None:
+        with _on("bitlinear_backward_weight_codes", stream, grad_y):
+            return bitlinear_backward_weight_codes(grad_y, xq, scale, out_dtype, grad_w)
+    where = "bitlinear_backward_weight_codes"
+    (M, N), dtype, dev, gy_at = _lead(where, "grad_y", grad_y)
+    if xq.dim() != 2:
+        _refuse(where, f"xq has shape {tuple(xq.shape)}")
+    K = xq.shape[1]
+    out_dtype = _out_dtype(where, out_dtype, grad_w)
+    if grad_w is None:
+        grad_w = torch.empty(N, K, dtype=out_dtype, device=grad_y.device)
+    _run(where, dev, _lib.bitlinear_backward_weight_codes,
+         (gy_at, _code(dtype), _addr(where, "xq", xq, (M, K), torch.int8, dev),
+          _addr(where, "scale", scale, (M,), _f32, dev), M, N, K,
+          _addr(where, "grad_w", grad_w, (N, K), out_dtype, dev), _code(out_dtype)))
+    return grad_w
+
+
+def bitlinear_backward_input_segmented(grad_y: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor,
+                                       seg_rows, K: int, layout="2bit", out_dtype=None,
+                                       grad_x: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """grad_x [M, K] of the input that a stack of matrices shares (seg_rows: N, or the
+    row counts; gammas[s] each; out_dtype: grad_x's type by default, then fp32)."""
+    if stream is not None:
+        with _on("bitlinear_backward_input_segmented", stream, grad_y):
+            return bitlinear_backward_input_segmented(grad_y, packed, gammas, seg_rows, K, layout, out_dtype, grad_x)
+    where = "bitlinear_backward_input_segmented"
+    lay = _one_of(where, "layout", layout, LAYOUTS)
+    table, nseg, N = _segments(_rows_of(seg_rows))
+    (M, cols), dtype, dev, gy_at = _lead(where, "grad_y", grad_y)
+    if cols != N:
+        _refuse(where, f"grad_y has {cols} columns for {N} rows of weights")
+    if gammas.dtype is not _f32 or gammas.numel() < nseg or gammas.get_device() != dev or not gammas.is_contiguous():
+        _refuse(where, f"gammas holds {gammas.numel()} of {gammas.dtype} on {gammas.device} for {nseg} segments, "
+                       "or is not contiguous")
+    K = operator.index(K)
+    out_dtype = _out_dtype(where, out_dtype, grad_x)
+    if grad_x is None:
+        grad_x = torch.empty(M, K, dtype=out_dtype, device=grad_y.device)
+    _run(where, dev, _lib.bitlinear_backward_input_segmented,
+         (gy_at, _code(dtype), _addr(where, "packed", packed, (N, _row_bytes(K, lay)), torch.uint8, dev), lay,
+          gammas.data_ptr(), table, nseg, M, K, _addr(where, "grad_x", grad_x, (M, K), out_dtype, dev),
+          _code(out_dtype)))
+    return grad_x

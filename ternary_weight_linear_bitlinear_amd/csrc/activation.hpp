@@ -143,6 +143,57 @@ __device__ __forceinline__ void times_slope(float (&g)[C], const float (&z)[C], 
     }
 }
 
+// Gradients of act(z) u for the gradient g of it: u becomes g act(z) (u's), z
+// becomes g u act'(z) (z's). Value and slope share their exponential.
+__device__ __forceinline__ void gated_grad(float g, float &z, float &u, float a, float slope) {
+    z = g * u * slope;
+    u = g * a;
+}
+template <int C>
+__device__ __forceinline__ void gated_grads(const float (&g)[C], float (&z)[C], float (&u)[C], int act) {
+    switch (act) {
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) gated_grad(g[e], z[e], u[e], fmaxf(z[e], 0.0f), z[e] > 0.0f ? 1.0f : 0.0f);
+            break;
+        case kActRelu2:
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                const float r = fmaxf(z[e], 0.0f);
+                gated_grad(g[e], z[e], u[e], r * r, 2.0f * r);
+            }
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                const float p = sigmoid_fast(z[e]);
+                gated_grad(g[e], z[e], u[e], z[e] * p, p * __builtin_fmaf(z[e], 1.0f - p, 1.0f));
+            }
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                const float x = fabsf(z[e]), n = half_gauss(z[e]), c = 0.5f * erfc_sqrt2(x, n);
+                gated_grad(g[e], z[e], u[e], __builtin_fmaf(-x, c, fmaxf(z[e], 0.0f)),
+                           __builtin_fmaf(z[e] * kInvSqrt2Pi, n, z[e] < 0.0f ? c : 1.0f - c));
+            }
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                const float zz = fminf(z[e] * z[e], 1e4f);  // as in gelu_tanh_slope
+                const float p = gelu_tanh_gate(z[e], zz);
+                const float du = kGeluTanhC * __builtin_fmaf(3.0f * kGeluTanhA, zz, 1.0f);
+                gated_grad(g[e], z[e], u[e], z[e] * p, __builtin_fmaf(z[e] * p * (1.0f - p), du, p));
+            }
+            break;
+        default:
+#pragma unroll
+            for (int e = 0; e < C; ++e) gated_grad(g[e], z[e], u[e], z[e], 1.0f);
+            break;
+    }
+}
+
 #endif
 
 }  // namespace bl

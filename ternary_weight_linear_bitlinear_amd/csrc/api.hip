@@ -131,6 +131,18 @@ bool valid_epilogue(const bl::EpilogueArgs &ep) {
     return aligned16(ep.bias) && aligned16(ep.residual) && aligned16(ep.z);  // NULL is aligned
 }
 
+// A stack of two matrices of F rows, and what must hold of a gated epilogue's operands.
+bool make_pair(const float *gammas, int64_t F, bl::GammaMap &gm) {
+    const int64_t rows[2] = {F, F};
+    int64_t N = 0;
+    return make_segments(gammas, rows, 2, gm, N);
+}
+bool valid_gated(const bl::GatedArgs &ga) {
+    if (ga.act < 0 || ga.act >= bl::kActCount || !valid_dtype(ga.bias_dtype)) return false;
+    if ((ga.codes != nullptr) != (ga.code_scale != nullptr)) return false;
+    return aligned16(ga.bias) && aligned16(ga.z) && aligned16(ga.codes) && aligned16(ga.code_scale);
+}
+
 // One norm of the block norm: kind, and parameters only with a norm.
 bool valid_norm(const bl::NormSide &s) {
     if (s.kind < bl::kNormNone || s.kind > bl::kNormLayer) return false;
@@ -390,6 +402,161 @@ bl_status bitlinear_epilogue_backward(const void *grad_y, int gy_dtype, const vo
     return launched(bl::launch_epilogue_backward(a, s));
 }
 
+bl_status bitlinear_forward_gated(const int8_t *xq, const float *scale, const uint8_t *packed,
+                                  int layout, const float *gammas, int64_t F, int64_t M, int64_t K,
+                                  const void *bias, int bias_dtype, int act, void *z,
+                                  int8_t *codes, float *code_scale, void *y, int y_dtype,
+                                  void *stream) {
+    bl::GammaMap gm;
+    const bl::GatedArgs ga{bias, bias_dtype, act, z, codes, code_scale, F};
+    if (!make_pair(gammas, F, gm) || !valid_gated(ga)) return BL_ERR_INVALID_ARG;
+    if (!valid_layout(layout) || !valid_dtype(y_dtype)) return BL_ERR_INVALID_ARG;
+    if (M < 0 || K < 1 || K > kMaxK || M > 65535LL * 128) return BL_ERR_INVALID_ARG;
+    if (M == 0) return BL_OK;
+    if (!xq || !scale || !packed || !gammas || !y) return BL_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(scale) || !aligned16(packed) || !aligned4(gammas) ||
+        !aligned16(y))
+        return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!codes && bl::skinny_handles(M, 2 * F, K, layout))
+        return launched(
+            bl::launch_gated_skinny(xq, scale, packed, layout, gm, M, K, y, y_dtype, ga, s));
+    const auto gemm = layout == BL_PACK_2BIT    ? bl::launch_gated_gemm_2bit
+                      : layout == BL_PACK_BASE3 ? bl::launch_gated_gemm_base3
+                                                : bl::launch_gated_gemm_1bit;
+    return launched(gemm(xq, scale, packed, gm, M, K, y, y_dtype, ga, s));
+}
+
+bl_status bitlinear_linear_gated(const void *x, int x_dtype, const uint8_t *packed, int layout,
+                                 const float *gammas, int64_t F, int64_t M, int64_t K,
+                                 const void *bias, int bias_dtype, int act, void *z, void *y,
+                                 int y_dtype, void *stream) {
+    bl::GammaMap gm;
+    const bl::GatedArgs ga{bias, bias_dtype, act, z, nullptr, nullptr, F};
+    if (!make_pair(gammas, F, gm) || !valid_gated(ga)) return BL_ERR_INVALID_ARG;
+    if (!valid_dtype(x_dtype) || !valid_layout(layout) || !valid_dtype(y_dtype))
+        return BL_ERR_INVALID_ARG;
+    if (M < 0 || K < 1 || K > kMaxK) return BL_ERR_INVALID_ARG;
+    if (M > bl::fused_decode_max_m()) return BL_ERR_UNSUPPORTED;
+    if (M == 0) return BL_OK;
+    if (!x || !packed || !gammas || !y) return BL_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(packed) || !aligned4(gammas) || !aligned16(y))
+        return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    return launched(bl::launch_gated_linear(x, x_dtype, packed, layout, gm, M, K, y, y_dtype, ga,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F) {
+    if (M < 1 || F < 1 || 2 * M > kMaxDim || 2 * F > kMaxDim) return 0;
+    return (size_t)(bl::gated_grad_parts(M, F) * 2 * F) * sizeof(float);
+}
+
+bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void *z, int z_dtype,
+                                   const int8_t *codes, const float *code_scale, int act,
+                                   int64_t M, int64_t F, void *grad_z, int gz_dtype,
+                                   float *grad_bias, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    if (M < 0 || F < 0 || M > kMaxDim / 2 || F > kMaxDim / 2) return BL_ERR_INVALID_ARG;
+    if (!valid_dtype(gy_dtype) || !valid_dtype(z_dtype) || !valid_dtype(gz_dtype))
+        return BL_ERR_INVALID_ARG;
+    if (act < 0 || act >= bl::kActCount) return BL_ERR_INVALID_ARG;
+    if (!aligned16(grad_y) || !aligned16(z) || !aligned16(codes) || !aligned16(code_scale) ||
+        !aligned16(grad_z) || !aligned16(grad_bias) || !aligned16(workspace))
+        return BL_ERR_INVALID_ARG;
+    if (F == 0) return BL_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M > 0) {
+        if (!grad_y || (codes != nullptr) != (code_scale != nullptr) ||
+            (z != nullptr) == (codes != nullptr))
+            return BL_ERR_INVALID_ARG;
+        if (!grad_z && !grad_bias) return BL_ERR_INVALID_ARG;
+        if (grad_bias &&
+            (!workspace || workspace_bytes < bitlinear_gated_backward_workspace_bytes(M, F)))
+            return BL_ERR_INVALID_ARG;
+    } else if (!grad_bias) {
+        return BL_OK;
+    }
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    if (M == 0) return launched(bl::launch_zero_f32(grad_bias, 2 * F, s));
+    const bl::GatedGradArgs a{grad_y,    z,        codes,    code_scale, grad_z,
+                              grad_bias, static_cast<float *>(workspace),
+                              gy_dtype,  z_dtype,  gz_dtype, act,        M, F};
+    return launched(bl::launch_gated_backward(a, s));
+}
+
+int64_t bitlinear_checkpoint_groups(int64_t K) { return K < 1 ? 0 : bl::checkpoint_groups(K); }
+
+bl_status bitlinear_checkpoint(const void *x, int x_dtype, int64_t M, int64_t K, int8_t *codes,
+                               float *scale, void *stream) {
+    if (M < 0 || K < 1 || M > kMaxDim || K > kMaxDim || !valid_dtype(x_dtype))
+        return BL_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return BL_ERR_INVALID_ARG;
+    if (M == 0) return BL_OK;
+    if (!x || !codes || !scale) return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    return launched(bl::launch_checkpoint(x, x_dtype, M, K, codes, scale,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_checkpoint_restore(const int8_t *codes, const float *scale, int64_t M, int64_t K,
+                                       void *y, int y_dtype, void *stream) {
+    if (M < 0 || K < 1 || M > kMaxDim || K > kMaxDim || !valid_dtype(y_dtype))
+        return BL_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scale) || !aligned16(y)) return BL_ERR_INVALID_ARG;
+    if (M == 0) return BL_OK;
+    if (!codes || !scale || !y) return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    return launched(bl::launch_checkpoint_restore(codes, scale, M, K, y, y_dtype,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
+                                          const float *scale, int64_t M, int64_t N, int64_t K,
+                                          void *grad_w, int gw_dtype, void *stream) {
+    if (M < 0 || N < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return BL_ERR_INVALID_ARG;
+    if (!valid_dtype(gy_dtype) || !valid_dtype(gw_dtype)) return BL_ERR_INVALID_ARG;
+    if (!aligned16(grad_y) || !aligned16(xq) || !aligned16(scale) || !aligned16(grad_w))
+        return BL_ERR_INVALID_ARG;
+    if (N == 0) return BL_OK;
+    if (!grad_w || (M > 0 && (!grad_y || !xq || !scale))) return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M == 0) return launched(bl::launch_zero(grad_w, gw_dtype, N * K, s));
+    return launched(bl::launch_backward_weight_codes(grad_y, gy_dtype, xq, scale, M, N, K, grad_w,
+                                                     gw_dtype, s));
+}
+
+bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
+                                             const uint8_t *packed, int layout,
+                                             const float *gammas, const int64_t *seg_rows, int nseg,
+                                             int64_t M, int64_t K, void *grad_x, int gx_dtype,
+                                             void *stream) {
+    bl::GammaMap gm;
+    int64_t N = 0;
+    if (!make_segments(gammas, seg_rows, nseg, gm, N)) return BL_ERR_INVALID_ARG;
+    if (M < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return BL_ERR_INVALID_ARG;
+    if (!valid_dtype(gy_dtype) || !valid_dtype(gx_dtype) || !valid_layout(layout))
+        return BL_ERR_INVALID_ARG;
+    if (M == 0) return BL_OK;
+    if (!grad_y || !packed || !gammas || !grad_x) return BL_ERR_INVALID_ARG;
+    if (!aligned16(grad_y) || !aligned16(packed) || !aligned4(gammas) || !aligned16(grad_x))
+        return BL_ERR_INVALID_ARG;
+    bl_status st = device_ok();
+    if (st != BL_OK) return st;
+    return launched(bl::launch_backward_input_segmented(grad_y, gy_dtype, packed, layout, gm, M, N,
+                                                        K, grad_x, gx_dtype,
+                                                        static_cast<hipStream_t>(stream)));
+}
+
 bl_status bitlinear_block_norm(const void *h, int h_dtype, const void *block, int x_dtype,
                                float res_scale, const void *gate, int gate_kind, int post_kind,
                                const void *post_weight, const void *post_bias, float post_eps,
@@ -525,7 +692,7 @@ const char *bitlinear_status_string(int status) {
     }
 }
 
-int bitlinear_version(void) { return (1 << 16) | 2; }
+int bitlinear_version(void) { return (1 << 16) | 3; }
 
 const char *bitlinear_source_hash(void) { return BL_SOURCE_HASH; }
 

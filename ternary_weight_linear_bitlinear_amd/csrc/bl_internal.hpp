@@ -192,7 +192,56 @@ BL_EPILOGUE_GEMM(launch_epilogue_gemm_2bit);
 BL_EPILOGUE_GEMM(launch_epilogue_gemm_base3);
 BL_EPILOGUE_GEMM(launch_epilogue_gemm_1bit);
 #undef BL_EPILOGUE_GEMM
-// Backward of that epilogue (epilogue.hip): grad_z = grad_y * act'(z), the
+// ---- gated products (skinny_gated.hip, gemm_gated_*.hip) -------------------
+// y = act(gate) * up over a stack of two matrices of F rows; the launchers take N
+// = 2F weight rows.
+constexpr int64_t kCheckpointGroup = 64;  // columns that share a scale
+constexpr int64_t checkpoint_groups(int64_t K) { return (K + kCheckpointGroup - 1) / kCheckpointGroup; }
+struct GatedArgs {
+    const void *bias;  // [2F], bias_dtype; NULL = none
+    int bias_dtype;
+    int act;
+    void *z;            // [M, 2F] of y's type, or NULL
+    int8_t *codes;      // [2M, F] and
+    float *code_scale;  // [2M, checkpoint_groups(F)], or both NULL: tiled products only
+    int64_t F;
+};
+hipError_t launch_gated_skinny(const int8_t *xq, const float *scale, const uint8_t *packed,
+                               int layout, const GammaMap &gamma, int64_t M, int64_t K, void *y,
+                               int y_dtype, const GatedArgs &ga, hipStream_t stream);
+hipError_t launch_gated_linear(const void *x, int x_dtype, const uint8_t *packed, int layout,
+                               const GammaMap &gamma, int64_t M, int64_t K, void *y, int y_dtype,
+                               const GatedArgs &ga, hipStream_t stream);
+#define BL_GATED_GEMM(NAME)                                                                    \
+    hipError_t NAME(const int8_t *xq, const float *scale, const uint8_t *packed,               \
+                    const GammaMap &gamma, int64_t M, int64_t K, void *y, int y_dtype,         \
+                    const GatedArgs &ga, hipStream_t stream)
+BL_GATED_GEMM(launch_gated_gemm_2bit);
+BL_GATED_GEMM(launch_gated_gemm_base3);
+BL_GATED_GEMM(launch_gated_gemm_1bit);
+#undef BL_GATED_GEMM
+// Backward of the gated epilogue (gated.hip).
+struct GatedGradArgs {
+    const void *grad_y;         // [M, F]
+    const void *z;              // [M, 2F], z_dtype, or NULL: then
+    const int8_t *codes;        // [2M, F] and
+    const float *code_scale;    // [2M, checkpoint_groups(F)]
+    void *grad_z;               // [M, 2F], or NULL
+    float *grad_bias;           // [2F], or NULL
+    float *workspace;           // column partials, [gated_grad_parts(M, F), 2F]
+    int gy_dtype, z_dtype, gz_dtype, act;
+    int64_t M, F;
+};
+int64_t gated_grad_parts(int64_t M, int64_t F);
+hipError_t launch_gated_backward(const GatedGradArgs &a, hipStream_t stream);
+
+// ---- activations kept in 8 bits (checkpoint.hip) ---------------------------
+hipError_t launch_checkpoint(const void *x, int x_dtype, int64_t M, int64_t K, int8_t *codes,
+                             float *scale, hipStream_t stream);
+hipError_t launch_checkpoint_restore(const int8_t *codes, const float *scale, int64_t M, int64_t K,
+                                     void *y, int y_dtype, hipStream_t stream);
+
+// Backward of the extended epilogue (epilogue.hip): grad_z = grad_y * act'(z), the
 // column sums of grad_z, res_scale * grad_y.
 struct EpilogueGradArgs {
     const void *grad_y, *z;
@@ -204,6 +253,8 @@ struct EpilogueGradArgs {
 };
 int64_t epilogue_grad_parts(int64_t M, int64_t N);  // partial sums per column in the workspace
 hipError_t launch_epilogue_backward(const EpilogueGradArgs &a, hipStream_t stream);
+// out[n] = sum over runs of part[run, n], in fp64 (epilogue.hip).
+hipError_t launch_run_sums(const float *part, float *out, int64_t N, int64_t runs, hipStream_t stream);
 
 // ---- norms around a block (norm.hip) --------------------------------------
 constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
@@ -255,7 +306,17 @@ hipError_t launch_backward_input(const void *grad_y, bool grad_y_f32, const uint
 // grad_w [N, K] fp32 = grad_y^T ([M, N]) x x ([M, K]), both bf16, or both fp32 when f32.
 hipError_t launch_backward_weight(const void *grad_y, const void *x, bool f32, int64_t M,
                                   int64_t N, int64_t K, float *grad_w, hipStream_t stream);
+// ---- backward products from codes and over stacks (backward_codes.hip) ----
+// grad_w [N, K] = sum_m grad_y[m, n] * (scale[m] / 127) * xq[m, k].
+hipError_t launch_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
+                                        const float *scale, int64_t M, int64_t N, int64_t K,
+                                        void *grad_w, int gw_dtype, hipStream_t stream);
+// grad_x [M, K] = sum over segments of gamma_s * grad_y_s [M, rows_s] . codes_s.
+hipError_t launch_backward_input_segmented(const void *grad_y, int gy_dtype, const uint8_t *packed,
+                                           int layout, const GammaMap &gamma, int64_t M, int64_t N,
+                                           int64_t K, void *grad_x, int gx_dtype, hipStream_t stream);
 // out[0 : count) = 0 (a kernel, so it can be captured in a graph).
 hipError_t launch_zero_f32(float *out, int64_t count, hipStream_t stream);
+hipError_t launch_zero(void *out, int dtype, int64_t count, hipStream_t stream);
 
 }  // namespace bl

@@ -225,6 +225,18 @@ __device__ __forceinline__ float wave_max0_dpp(float v) {  // of values >= 0
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Maximum over each aligned group of eight lanes (all active), in every lane of it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xf,
+                                                      0xf, false));
+}
+__device__ __forceinline__ float max8_dpp(float v) {
+    v = fmaxf(v, dpp_of<0xB1>(v));   // quad_perm 1, 0, 3, 2
+    v = fmaxf(v, dpp_of<0x4E>(v));   // quad_perm 2, 3, 0, 1
+    return fmaxf(v, dpp_of<0x141>(v));  // row_half_mirror: lane i of eight reads 7 - i
+}
+
 // Expand one 32-bit word of the 2-bit layout (16 codes) into four dwords of
 // signed code bytes in natural order: dword j holds codes 4j..4j+3. The field
 // u = (word >> 2j) & 0x03030303 is mapped to c = u - 1 by a byte permute whose

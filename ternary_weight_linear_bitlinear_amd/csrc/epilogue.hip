@@ -128,6 +128,12 @@ __global__ __launch_bounds__(kThreads) void epilogue_grad_sums_kernel(const floa
 
 }  // namespace
 
+hipError_t launch_run_sums(const float *part, float *out, int64_t N, int64_t runs, hipStream_t stream) {
+    hipLaunchKernelGGL(epilogue_grad_sums_kernel, dim3((unsigned)((N + 31) / 32)), dim3(kThreads), 0,
+                       stream, part, out, N, runs);
+    return hipGetLastError();
+}
+
 int64_t epilogue_grad_parts(int64_t M, int64_t N) {
     if (M <= kOneRunRows) return 1;
     const int64_t wide = (N + 8 * kWide - 1) / (8 * kWide);
@@ -165,9 +171,7 @@ hipError_t launch_epilogue_backward(const EpilogueGradArgs &a, hipStream_t strea
                     e = a.N % 8 == 0 ? pieces(std::true_type{}) : pieces(std::false_type{});
                 }
                 if (e != hipSuccess || !a.grad_bias || runs == 1) return e;
-                hipLaunchKernelGGL(epilogue_grad_sums_kernel, dim3((unsigned)((a.N + 31) / 32)),
-                                   dim3(kThreads), 0, stream, a.workspace, a.grad_bias, a.N, runs);
-                return hipGetLastError();
+                return launch_run_sums(a.workspace, a.grad_bias, a.N, runs, stream);
             });
         });
     });

@@ -18,7 +18,8 @@ namespace bl {
 // The plain dequant epilogue: the products store gamma * scale / 127 * acc
 // (and the sums) themselves.
 struct NoEpilogue {
-    static constexpr bool kActive = false;
+    static constexpr bool kActive = false, kGated = false;
+    static constexpr int kPair = 1;  // weight rows behind an output column
     NoEpilogue from_col(int64_t) const { return {}; }
 };
 
@@ -26,7 +27,8 @@ struct NoEpilogue {
 // column. residual and z are laid out and typed as y.
 template <typename YT>
 struct Epilogue {
-    static constexpr bool kActive = true;
+    static constexpr bool kActive = true, kGated = false;
+    static constexpr int kPair = 1;
     const void *bias;    // [N] fp32, or bf16 when bias_bf16; NULL = none
     const YT *residual;  // NULL = none; may be y itself
     YT *z;               // NULL = not stored
@@ -171,6 +173,82 @@ struct Epilogue {
 #endif
 };
 
+// Operands of the gated epilogue. The packed matrix is a stack of two, gate rows
+// 0 .. F - 1 and up rows F .. 2F - 1, and output column f is
+//   z_h = gamma_h * scale / 127 * acc[h F + f] + bias[h F + f],  h = 0 (gate), 1 (up)
+//   y[f] = act(z_0) * z_1
+// in fp32, rounded once to y's type; z [M, 2F] is laid out as the stack's output.
+// A launch's N counts weight rows, two for each output column; how a tile of them
+// is dealt to the halves is up to the kernel (both halves of a column in one tile).
+template <typename YT>
+struct GatedEpilogue {
+    static constexpr bool kActive = true, kGated = true;
+    static constexpr int kPair = 2;
+    const void *bias;   // [2F] fp32, or bf16 when bias_bf16; NULL = none
+    YT *z;              // NULL = not stored
+    int8_t *codes;      // [2M, F]: z in 8 bits, rows 2m (gate) and 2m + 1 (up); NULL = not kept
+    float *code_scale;  // [2M, groups]
+    int64_t F, groups;  // columns in all; checkpoint groups of a row
+    int64_t up;         // bytes from a gate row to its up row
+    int64_t col0;       // the launch's first output column
+    int act;
+    int bias_bf16;
+
+    // the same operands seen from weight row `off` of the launch on
+    GatedEpilogue from_col(int64_t off) const {
+        GatedEpilogue e = *this;
+        e.col0 += off / 2;
+        return e;
+    }
+
+#if defined(__HIPCC__)
+    using Ep = Epilogue<YT>;
+    __device__ __forceinline__ float bias_at(int64_t n) const {
+        return bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(bias)[n])
+                         : static_cast<const float *>(bias)[n];
+    }
+    // Bias of columns n .. n + C - 1 of half h (0 past F, and without a bias); n is a
+    // multiple of C, counted over all columns.
+    template <int C>
+    __device__ __forceinline__ void load_bias(int h, int64_t n, float (&b)[C]) const {
+        if (bias && n + C <= F && F % C == 0) {
+            if (bias_bf16) Epilogue<uint16_t>::load(static_cast<const uint16_t *>(bias) + h * F + n, b);
+            else Epilogue<float>::load(static_cast<const float *>(bias) + h * F + n, b);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < C; ++e) b[e] = bias && n + e < F ? bias_at(h * F + n + e) : 0.f;
+    }
+    // C consecutive outputs of token m from both halves' dequantised products g and u,
+    // which leave as the pre-activations: columns n .. n + C - 1 of all (those below F);
+    // yt[e] is column n + e of y. vec: all C are below F, and F and yt are aligned to C
+    // outputs.
+    template <int C>
+    __device__ __forceinline__ void finish(float (&g)[C], float (&u)[C], const float (&bg)[C],
+                                           const float (&bu)[C], int64_t m, int64_t n, bool vec,
+                                           YT *yt) const {
+        if (bias) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                g[e] += bg[e];
+                u[e] += bu[e];
+            }
+        }
+        if (z) {
+            Ep::put(z + m * 2 * F + n, g, 0, n, F, vec);
+            Ep::put(z + m * 2 * F + F + n, u, 0, n, F, vec);
+        }
+        float v[C];
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = g[e];
+        activate_all(v, act);
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] *= u[e];
+        Ep::put(yt, v, 0, n, F, vec);
+    }
+#endif
+};
+
 // How a product's kernel takes y: the plain epilogue never reads what it writes,
 // the extended one may be given y as its residual.
 template <typename YT, typename E>
@@ -180,6 +258,12 @@ template <typename YT>
 Epilogue<YT> make_epilogue(const EpilogueArgs &a) {
     return Epilogue<YT>{a.bias, static_cast<const YT *>(a.residual), static_cast<YT *>(a.z),
                         a.res_scale, a.act, a.bias_dtype == kBF16};
+}
+template <typename YT>
+GatedEpilogue<YT> make_gated(const GatedArgs &a, int64_t row_bytes) {
+    return GatedEpilogue<YT>{a.bias, static_cast<YT *>(a.z), a.codes, a.code_scale, a.F,
+                             checkpoint_groups(a.F), a.F * row_bytes, 0, a.act,
+                             a.bias_dtype == kBF16};
 }
 
 }  // namespace bl

@@ -285,6 +285,88 @@ struct RowEpilogue {
     }
 };
 
+// The same for the gated epilogue: a tile's BN weight rows are gate rows col ..
+// col + BN / 2 - 1 and then the same up rows, so that a thread finishes eight
+// output columns of a token from a piece of either half. Kept in 8 bits, eight
+// threads side by side hold a checkpoint group of 64 columns (tiles begin at
+// multiples of 64) and take its maximum across lanes.
+template <int BN, int T, typename YT>
+struct GatedRows {
+    static constexpr int kPieces = BN / 16, kStep = T / kPieces;
+    static_assert(T % kPieces == 0 && kPieces % 8 == 0 && (BN / 2) % kCheckpointGroup == 0,
+                  "whole rows a step, whole groups a tile");
+    const GatedEpilogue<YT> &ep;
+    const LdsFloats rowf;
+    const int64_t m0, col, M, F, ld;  // col: counted from the launch's first, below F
+    YT *y;
+    bool vec;
+    int row0, piece;
+    float gam[2], bg[8], bu[8];
+    __device__ __forceinline__ GatedRows(const GatedEpilogue<YT> &ep_, const GammaMap &,
+                                         const float (&gs)[kMaxSegments], float *rowf_, int64_t m0_,
+                                         int64_t n0, int64_t M_, int64_t N_, int64_t ld_, YT *y_)
+        : ep(ep_), rowf((LdsFloats)rowf_), m0(m0_), col(n0 / 2 + (threadIdx.x % kPieces) * 8), M(M_),
+          F(N_ / 2), ld(ld_), y(y_) {
+        row0 = threadIdx.x / kPieces;
+        piece = threadIdx.x % kPieces;
+        vec = col + 8 <= F && ep.F % 8 == 0;
+        gam[0] = gs[0];
+        gam[1] = gs[1];
+        ep.load_bias(0, ep.col0 + col, bg);
+        ep.load_bias(1, ep.col0 + col, bu);
+    }
+    __device__ __forceinline__ void keep(const float (&v)[8], int64_t row) const {
+        const int64_t c = ep.col0 + col;
+        float a[8], m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = vec || c + e < ep.F ? v[e] : 0.f;
+            m = fmaxf(m, fabsf(a[e]));
+        }
+        const float s = fmaxf(max8_dpp(m), 1e-6f), r = 1.0f / s;
+        if (c >= ep.F) return;
+        const uint2 q = make_uint2(quant4(a[0], a[1], a[2], a[3], s, r), quant4(a[4], a[5], a[6], a[7], s, r));
+        int8_t *p = ep.codes + row * ep.F + c;
+        if (vec) {
+            *reinterpret_cast<uint2 *>(p) = q;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < ep.F) p[e] = (int8_t)((e < 4 ? q.x : q.y) >> (8 * (e % 4)));
+        }
+        if (threadIdx.x % 8 == 0) ep.code_scale[row * ep.groups + c / kCheckpointGroup] = s;
+    }
+    template <typename B>
+    __device__ __forceinline__ void run(B buf, int first, int frags) const {
+        if (!ep.codes && col >= F) return;  // (a group's eight threads stay together)
+#pragma unroll 2
+        for (int rr = row0; rr < 32 * frags; rr += kStep) {
+            const int64_t m = m0 + first + rr;
+            if (m >= M) return;
+            const int r = rr % 32;
+            const LdsBytes p = buf(rr / 32);
+            const v4i g0 = *(LdsV4i)(p + frag_slot<BN>(r, 2 * piece));
+            const v4i g1 = *(LdsV4i)(p + frag_slot<BN>(r, 2 * piece + 1));
+            const v4i u0 = *(LdsV4i)(p + frag_slot<BN>(r, BN / 8 + 2 * piece));
+            const v4i u1 = *(LdsV4i)(p + frag_slot<BN>(r, BN / 8 + 2 * piece + 1));
+            const float f = rowf[first + rr], fg = gam[0] * f, fu = gam[1] * f;
+            float g[8], u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                g[e] = (float)(e < 4 ? g0[e] : g1[e - 4]) * fg;
+                u[e] = (float)(e < 4 ? u0[e] : u1[e - 4]) * fu;
+            }
+            ep.finish(g, u, bg, bu, m, ep.col0 + col, vec, y + m * ld + col);
+            if (ep.codes) {
+                keep(g, 2 * m);
+                keep(u, 2 * m + 1);
+            }
+        }
+    }
+};
+template <int BN, int T, typename YT, typename E>
+using RowsOf = std::conditional_t<E::kGated, GatedRows<BN, T, YT>, RowEpilogue<BN, T, YT, E>>;
+
 template <int LAYOUT, int BM, int BN, int WM, int WN, int DIST, int KG, int KMODE,
           typename YT, typename E>
 __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E &ep) {
@@ -337,6 +419,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
     const uint8_t *b_src[C::FJ];
 #pragma unroll
     for (int j = 0; j < C::FJ; ++j) {
+        if constexpr (E::kGated) {
+            static_assert((BN / 2) % 32 == 0, "a fragment holds rows of one half");
+            const int v = wn * (BN / WN) + j * 32, h = v >= BN / 2;
+            const int64_t n = n0 / 2 + v - h * (BN / 2) + frow;
+            b_src[j] = packed + (n < N / 2 ? n : 0) * rb + h * ep.up;
+            continue;
+        }
         const int64_t n = n0 + wn * (BN / WN) + j * 32 + frow;
         b_src[j] = packed + (n < N ? n : 0) * rb;
     }
@@ -629,7 +718,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs<YT> &g, int t, const E 
         constexpr int FP = C::kEpiFrags;  // fragment rows staged at a time
         __shared__ float rowf[BM];
         stage_row_factors<BM, kThreads>(rowf, gm, gs[0], scale, m0, M);
-        const RowEpilogue<BN, kThreads, YT, E> rows(ep, gm, gs, rowf, m0, n0, M, N, ldy, y);
+        const RowsOf<BN, kThreads, YT, E> rows(ep, gm, gs, rowf, m0, n0, M, N, ldy, y);
         if constexpr (KG > 1) lds_barrier();  // the other groups' sums have been read
 #pragma unroll
         for (int i0 = 0; i0 < C::FI; i0 += FP) {
@@ -769,6 +858,15 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_epilogue_kernel(const 
     gemm_tile<LAYOUT, BM, BN, WM, WN, DIST, KG, KMODE, YT>(g, t, ep);
 }
 
+template <int LAYOUT, int BM, int BN, int WM, int WN, int DIST, int KG, int KMODE,
+          typename YT>
+__global__ __launch_bounds__(64 * WM * WN * KG) void gemm_gated_kernel(const GemmArgs<YT> g,
+                                                                       const GatedEpilogue<YT> ep) {
+    const int t = xcd_tile(blockIdx.x, g.tiles_m * g.tiles_n);
+    if (t < 0) return;
+    gemm_tile<LAYOUT, BM, BN, WM, WN, DIST, KG, KMODE, YT>(g, t, ep);
+}
+
 // BM x 256 tiles (BM = 256, 128 or 96) of 2-bit or 1-bit rows of whole k-tiles,
 // bf16 out, tiles whole in N: the activation tile reaches LDS by direct-to-LDS
 // loads (16 bytes a lane, no staging registers), three k-tiles deep, and the
@@ -845,7 +943,10 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
     const int64_t ktiles = rb / C::LB / 2;  // whole k-tiles (the caller checks)
 
     // this lane's weight row and activation rows
-    const uint8_t *bsrc = g.packed + (n0 + wave * 32 + frow) * rb;
+    // (gated: gate rows in waves 0..3, the same up rows in waves 4..7)
+    const uint8_t *bsrc;
+    if constexpr (E::kGated) bsrc = g.packed + (n0 / 2 + wave % 4 * 32 + frow) * rb + wave / 4 * ep.up;
+    else bsrc = g.packed + (n0 + wave * 32 + frow) * rb;
     // (sized for the largest J: an array sized by J would make the load builtin's
     // arguments depend on BM, which the host compilation pass rejects)
     const int8_t *asrc[4];
@@ -947,7 +1048,7 @@ __device__ __forceinline__ void gemm_tile_dma(const GemmArgs<YT> &g, int t, cons
         load_gammas(gm, gse);
         __shared__ float rowf[BM];
         stage_row_factors<BM, 512>(rowf, gm, gse[0], scale, m0, M);
-        const RowEpilogue<256, 512, YT, E> rows(ep, gm, gse, rowf, m0, n0, M, g.N, ldy, y);
+        const RowsOf<256, 512, YT, E> rows(ep, gm, gse, rowf, m0, n0, M, g.N, ldy, y);
         int8_t *const bufs[4] = {dma_s0, dma_s1, dma_s2, reinterpret_cast<int8_t *>(dma_out)};
         static_assert(kDmaStage == 32 * 256 * 4 && 64 * kDmaOutRow >= kDmaStage, "a fragment row fits");
 #pragma unroll
@@ -1059,6 +1160,28 @@ __global__ __launch_bounds__(512) void gemm_dma_pair_epilogue_kernel(
     }
 }
 
+template <int LAYOUT, int BM, typename YT>
+__global__ __launch_bounds__(512) void gemm_dma_gated_kernel(const GemmArgs<YT> g,
+                                                             const GatedEpilogue<YT> ep) {
+    const int t = xcd_tile(blockIdx.x, g.tiles_m * g.tiles_n);
+    if (t < 0) return;
+    gemm_tile_dma<LAYOUT, BM, false, YT>(g, t, ep);
+}
+
+template <int LAYOUT, int BM2, typename YT>
+__global__ __launch_bounds__(512) void gemm_dma_pair_gated_kernel(
+    const GemmArgs<YT> g1, int blocks1, const GemmArgs<YT> g2, const GatedEpilogue<YT> ep1,
+    const GatedEpilogue<YT> ep2) {
+    const int b = blockIdx.x;
+    if (b < blocks1) {
+        const int t = xcd_tile(b, g1.tiles_m * g1.tiles_n);
+        if (t >= 0) gemm_tile_dma<LAYOUT, 256, false, YT>(g1, t, ep1);
+    } else {
+        const int t = xcd_tile(b - blocks1, g2.tiles_m * g2.tiles_n);
+        if (t >= 0) gemm_tile_dma<LAYOUT, BM2, false, YT>(g2, t, ep2);
+    }
+}
+
 // The direct-to-LDS tiles serve a launch when its columns are whole 256-wide
 // tiles, the rows hold whole k-tiles (2-bit, or 1-bit without padding codes)
 // and the output is bf16 with rows of whole 16-byte pieces.
@@ -1088,7 +1211,10 @@ hipError_t launch_gemm_dma(const int8_t *xq, const float *scale, const uint8_t *
         return hipSuccess;
     }
     if constexpr (LAYOUT != kLayoutBase3 && sizeof(YT) == 2) {
-        if constexpr (E::kActive) {
+        if constexpr (E::kGated) {
+            hipLaunchKernelGGL((gemm_dma_gated_kernel<LAYOUT, BM, YT>), dim3(blocks), dim3(512), 0, s,
+                               g, ep);
+        } else if constexpr (E::kActive) {
             if (gamma.nseg > 1)
                 hipLaunchKernelGGL((gemm_dma_epilogue_kernel<LAYOUT, BM, true, YT>), dim3(blocks),
                                    dim3(512), 0, s, g, ep);
@@ -1113,9 +1239,10 @@ hipError_t launch_gemm_dma_pair(const int8_t *xq, const float *scale, const uint
     const int64_t rb = row_bytes_of(LAYOUT, K);
     const int tm = (int)((M + 255) / 256), tm2 = (int)((M + BM2 - 1) / BM2);
     const int tn1 = (int)(n_main / 256), tn2 = (int)((N - n_main) / 256);
-    GemmArgs<YT> g1{xq, scale, packed, gamma, M, n_main, K, rb, tm, tn1, y, N, acc};
-    GemmArgs<YT> g2{xq, scale, packed + n_main * rb, gamma.from_row(n_main), M, N - n_main,
-                    K, rb, tm2, tn2, y + n_main, N, acc ? acc + n_main : nullptr};
+    constexpr int P = E::kPair;
+    GemmArgs<YT> g1{xq, scale, packed, gamma, M, n_main, K, rb, tm, tn1, y, N / P, acc};
+    GemmArgs<YT> g2{xq, scale, packed + n_main / P * rb, gamma.from_row(n_main), M, N - n_main,
+                    K, rb, tm2, tn2, y + n_main / P, N / P, acc ? acc + n_main : nullptr};
     g1.band = tile_band(tm, tn1, 256 * K, 256 * rb);
     g2.band = tile_band(tm2, tn2, BM2 * K, 256 * rb);
     const int blocks1 = (tm * tn1 + kXcds - 1) / kXcds * kXcds;
@@ -1129,7 +1256,10 @@ hipError_t launch_gemm_dma_pair(const int8_t *xq, const float *scale, const uint
     }
     if constexpr (LAYOUT != kLayoutBase3 && sizeof(YT) == 2) {
         const dim3 grid((unsigned)(blocks1 + blocks2));
-        if constexpr (E::kActive) {
+        if constexpr (E::kGated) {
+            hipLaunchKernelGGL((gemm_dma_pair_gated_kernel<LAYOUT, BM2, YT>), grid, dim3(512), 0, s, g1,
+                               blocks1, g2, ep, ep.from_col(n_main));
+        } else if constexpr (E::kActive) {
             const E ep2 = ep.from_col(n_main);
             if (gamma.nseg > 1)
                 hipLaunchKernelGGL((gemm_dma_pair_epilogue_kernel<LAYOUT, BM2, true, YT>), grid,
@@ -1146,6 +1276,21 @@ hipError_t launch_gemm_dma_pair(const int8_t *xq, const float *scale, const uint
         }
     }
     return hipGetLastError();
+}
+
+template <int LAYOUT, int KMODE, typename YT, int BM2>
+__global__ __launch_bounds__(512) void gemm_pair_gated_kernel(const GemmArgs<YT> g1, int blocks1,
+                                                              const GemmArgs<YT> g2,
+                                                              const GatedEpilogue<YT> ep1,
+                                                              const GatedEpilogue<YT> ep2) {
+    const int b = blockIdx.x;
+    if (b < blocks1) {
+        const int t = xcd_tile(b, g1.tiles_m * g1.tiles_n);
+        if (t >= 0) gemm_tile<LAYOUT, 256, 256, 1, 8, 2, 1, KMODE, YT>(g1, t, ep1);
+    } else {
+        const int t = xcd_tile(b - blocks1, g2.tiles_m * g2.tiles_n);
+        if (t >= 0) gemm_tile<LAYOUT, BM2, 256, 1, 8, 2, 1, KMODE, YT>(g2, t, ep2);
+    }
 }
 
 // The prefill shape in one launch: the first blocks cover the columns that
@@ -1211,7 +1356,9 @@ hipError_t launch_gemm_tile(const int8_t *xq, const float *scale, const uint8_t 
     static LdsFlag lds_flag[3];  // one per k-mode
     auto mode = [&](auto mode_c) {
         constexpr int KM = decltype(mode_c)::value;
-        if constexpr (E::kActive)
+        if constexpr (E::kGated)
+            return launch(gemm_gated_kernel<LAYOUT, BM, BN, WM, WN, DIST, KG, KM, YT>, &lds_flag[KM]);
+        else if constexpr (E::kActive)
             return launch(gemm_epilogue_kernel<LAYOUT, BM, BN, WM, WN, DIST, KG, KM, YT>,
                           &lds_flag[KM]);
         else
@@ -1325,9 +1472,10 @@ hipError_t launch_gemm_pair(const int8_t *xq, const float *scale, const uint8_t 
     const int64_t rb = row_bytes_of(LAYOUT, K);
     const int tm = (int)((M + 255) / 256), tm2 = (int)((M + BM2 - 1) / BM2);
     const int tn1 = (int)((n_main + 255) / 256), tn2 = (int)((N - n_main + 255) / 256);
-    GemmArgs<YT> g1{xq, scale, packed, gamma, M, n_main, K, rb, tm, tn1, y, N, acc};
-    GemmArgs<YT> g2{xq, scale, packed + n_main * rb, gamma.from_row(n_main), M, N - n_main,
-                    K, rb, tm2, tn2, y + n_main, N, acc ? acc + n_main : nullptr};
+    constexpr int P = E::kPair;
+    GemmArgs<YT> g1{xq, scale, packed, gamma, M, n_main, K, rb, tm, tn1, y, N / P, acc};
+    GemmArgs<YT> g2{xq, scale, packed + n_main / P * rb, gamma.from_row(n_main), M, N - n_main,
+                    K, rb, tm2, tn2, y + n_main / P, N / P, acc ? acc + n_main : nullptr};
     g1.band = tile_band(tm, tn1, 256 * K, 256 * rb);
     g2.band = tile_band(tm2, tn2, BM2 * K, 256 * rb);
     const int blocks1 = (tm * tn1 + kXcds - 1) / kXcds * kXcds;
@@ -1352,7 +1500,9 @@ hipError_t launch_gemm_pair(const int8_t *xq, const float *scale, const uint8_t 
     static LdsFlag lds_flag[3];  // one per k-mode
     auto mode = [&](auto mode_c) {
         constexpr int KM = decltype(mode_c)::value;
-        if constexpr (E::kActive)
+        if constexpr (E::kGated)
+            return launch(gemm_pair_gated_kernel<LAYOUT, KM, YT, BM2>, &lds_flag[KM]);
+        else if constexpr (E::kActive)
             return launch(gemm_pair_epilogue_kernel<LAYOUT, KM, YT, BM2>, &lds_flag[KM]);
         else
             return launch(gemm_pair_kernel<LAYOUT, KM, YT, BM2>, &lds_flag[KM]);
@@ -1369,6 +1519,8 @@ hipError_t launch_gemm_t(const int8_t *xq, const float *scale, const uint8_t *pa
                          const GammaMap &gamma, int64_t M, int64_t N, int64_t K, YT *y,
                          int32_t *acc, hipStream_t s, const E &ep) {
     constexpr int64_t kCUs = 256;
+    constexpr int P = E::kPair;
+    const int64_t ldy = N / P;
     const int64_t rb = row_bytes_of(LAYOUT, K);
     {
         const int64_t tm = (M + 255) / 256, tn = (N + 255) / 256;
@@ -1381,7 +1533,7 @@ hipError_t launch_gemm_t(const int8_t *xq, const float *scale, const uint8_t *pa
             // of 256, one column of tiles) leave no whole round: no 256 x 256
             // launch, all columns take the smaller tiles
             if (tn_main == 0)
-                return launch_gemm_cols<LAYOUT>(xq, scale, packed, gamma, M, N, K, y, N, acc, s,
+                return launch_gemm_cols<LAYOUT>(xq, scale, packed, gamma, M, N, K, y, ldy, acc, s,
                                                 ep);
             const int64_t n_main = tn_main * 256 < N ? tn_main * 256 : N;
             const int64_t n_rest = N - n_main;
@@ -1394,7 +1546,7 @@ hipError_t launch_gemm_t(const int8_t *xq, const float *scale, const uint8_t *pa
                 // 109.4 us on two boxes, 1-bit 91.3 -> 91.3 and 100.7 -> 99.0
                 // us, 2-bit within 1% either way)
                 const int64_t t_rest96 = ((M + 95) / 96) * ((n_rest + 255) / 256);
-                const bool dma = gemm_dma_fits<LAYOUT, YT>(N, K, N);
+                const bool dma = gemm_dma_fits<LAYOUT, YT>(N, K, ldy);
                 if (t_rest96 <= kCUs)
                     return dma ? launch_gemm_dma_pair<LAYOUT, 96>(xq, scale, packed, gamma, M, N,
                                                                   K, n_main, y, acc, s, ep)
@@ -1405,19 +1557,19 @@ hipError_t launch_gemm_t(const int8_t *xq, const float *scale, const uint8_t *pa
                            : launch_gemm_pair<LAYOUT, 128>(xq, scale, packed, gamma, M, N, K,
                                                            n_main, y, acc, s, ep);
             }
-            hipError_t e = gemm_dma_fits<LAYOUT, YT>(n_main, K, N)
+            hipError_t e = gemm_dma_fits<LAYOUT, YT>(n_main, K, ldy)
                                ? launch_gemm_dma<LAYOUT, 256>(xq, scale, packed, gamma, M, n_main,
-                                                              K, y, N, acc, s, ep)
+                                                              K, y, ldy, acc, s, ep)
                                : launch_gemm_tile<LAYOUT, 256, 256, 1, 8, 2>(
-                                     xq, scale, packed, gamma, M, n_main, K, y, N, acc, s, ep);
+                                     xq, scale, packed, gamma, M, n_main, K, y, ldy, acc, s, ep);
             if (e != hipSuccess || n_main == N) return e;
-            return launch_gemm_cols<LAYOUT>(xq, scale, packed + n_main * rb,
+            return launch_gemm_cols<LAYOUT>(xq, scale, packed + n_main / P * rb,
                                             gamma.from_row(n_main), M, N - n_main,
-                                            K, y + n_main, N, acc ? acc + n_main : nullptr, s,
+                                            K, y + n_main / P, ldy, acc ? acc + n_main : nullptr, s,
                                             ep.from_col(n_main));
         }
     }
-    return launch_gemm_cols<LAYOUT>(xq, scale, packed, gamma, M, N, K, y, N, acc, s,
+    return launch_gemm_cols<LAYOUT>(xq, scale, packed, gamma, M, N, K, y, ldy, acc, s,
                                                 ep);
 }
 

@@ -104,6 +104,35 @@ __device__ __forceinline__ void store_share(T *row, int j, const Share<J, VEC> &
     }
 }
 
+// Eight kept codes as loaded, with their group's scale: q * (scale / 127). A code
+// plus 128 is an unsigned byte, which the hardware converts without a shift, and
+// (q + 128) f - 128 f in one fused operation is q f rounded once.
+struct Kept8 {
+    uint2 a;
+    float s;
+    __device__ __forceinline__ void widen(float v[8]) const {
+        const float f = s / 127.0f, off = -128.0f * f;
+        const uint32_t w[2] = {a.x ^ 0x80808080u, a.y ^ 0x80808080u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = __builtin_fmaf((float)((w[e / 4] >> (8 * (e % 4))) & 0xFFu), f, off);
+    }
+};
+// One chunk (J = 1) of a kept row. `scale` holds the row's groups; `group` is the
+// chunk's own (of its first column, not of where an end chunk is loaded from).
+template <bool VEC>
+__device__ __forceinline__ void load_kept(const int8_t *row, const float *scale, int64_t group,
+                                          const Share<1, VEC> &sh, Kept8 &r) {
+    const int8_t *p = row + sh.start(0);
+    if constexpr (VEC) {
+        r.a = *reinterpret_cast<const uint2 *>(p);
+    } else {
+        const Bytes8 b = *reinterpret_cast<const Bytes8 *>(p);
+        r.a = make_uint2(b.w[0], b.w[1]);
+    }
+    r.s = scale[group];
+}
+
 // Calls go(float or uint16_t pointer) by a tensor's type.
 template <typename F>
 hipError_t typed(int dtype, F go) {

@@ -254,8 +254,39 @@ struct EpilogueAhead {
 };
 template <typename YT>
 struct NoEpilogueAhead {};
+
+// Gated products: a group of 16 weight rows is eight gate rows and the same eight
+// up rows, so that every launch shape and the dispatch by rows stay those of the
+// plain products. The matrix cores leave gate columns 4 g .. 4 g + 3 in lane group
+// g = 0, 1 and up columns 4 (g - 2) .. in g = 2, 3: lanes 32 apart exchange theirs.
+__device__ __forceinline__ int64_t gated_col(int64_t v) { return v / 16 * 8 + v % 8; }
+template <typename YT>
+struct GatedAhead {
+    __device__ __forceinline__ void fetch(const GatedEpilogue<YT> &, const void *, int64_t, int64_t,
+                                          int64_t) {}
+    // (all lanes of a token's sums take part; v: the lane's first weight row)
+    __device__ __forceinline__ void store(const GammaMap &, const float (&gs)[kMaxSegments], float scale,
+                                          const v4i tot, int64_t m, int64_t v, int64_t, YT *y,
+                                          const GatedEpilogue<YT> &ep) const {
+        const int half = (int)(v % 16) / 8;
+        const float f = gs[half] * (scale / 127.0f);
+        float a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = (float)tot[i] * f;
+            b[i] = __shfl_xor(a[i], 32, 64);
+        }
+        const int64_t n = gated_col(v);
+        if (half || n >= ep.F) return;
+        float bg[4], bu[4];
+        ep.load_bias(0, n, bg);
+        ep.load_bias(1, n, bu);
+        ep.finish(a, b, bg, bu, m, n, ep.F % 4 == 0, y + m * ep.F + n);
+    }
+};
 template <typename YT, typename E>
-using AheadOf = std::conditional_t<E::kActive, EpilogueAhead<YT>, NoEpilogueAhead<YT>>;
+using AheadOf = std::conditional_t<E::kGated, GatedAhead<YT>,
+                                   std::conditional_t<E::kActive, EpilogueAhead<YT>, NoEpilogueAhead<YT>>>;
 
 // RG row groups of 16 weight rows per workgroup share every activation read
 // from LDS (one operand load feeds RG matrix-core instructions); RG > 1 pays
@@ -320,6 +351,12 @@ __device__ __forceinline__ void skinny_block(
     bool row_ok[RG];
 #pragma unroll
     for (int q = 0; q < RG; ++q) {
+        if constexpr (E::kGated) {
+            const int64_t n = gated_col(n0 + 16 * q + r);
+            row_ok[q] = n < ep.F;
+            wrow[q] = packed + (n + r / 8 * ep.F) * rb;
+            continue;
+        }
         row_ok[q] = n0 + 16 * q + r < N;
         wrow[q] = packed + (n0 + 16 * q + r) * rb;
     }
@@ -519,6 +556,15 @@ __global__ __launch_bounds__(64 * KS) void skinny_epilogue_kernel(
                                                     ep);
 }
 
+template <int LAYOUT, int KS, int NSS, int RG, int MAXM, bool MR, typename YT>
+__global__ __launch_bounds__(64 * KS) void skinny_gated_kernel(
+    const int8_t *__restrict__ xq, const float *__restrict__ scale,
+    const uint8_t *__restrict__ packed, const GammaMap gm, int M, int64_t N,
+    int64_t K, int64_t rb, YT *__restrict__ y, const GatedEpilogue<YT> ep) {
+    skinny_block<LAYOUT, KS, NSS, RG, MAXM, MR, YT>(xq, scale, packed, gm, M, N, K, rb, y, nullptr,
+                                                    ep);
+}
+
 template <int LAYOUT, int KS, int NSS, int RG, int MAXM, typename YT, typename E>
 hipError_t launch_skinny_t(const int8_t *xq, const float *scale, const uint8_t *packed,
                            const GammaMap &gamma, int64_t M, int64_t N, int64_t K, YT *y,
@@ -551,7 +597,10 @@ hipError_t launch_skinny_t(const int8_t *xq, const float *scale, const uint8_t *
         return hipGetLastError();
     };
     static LdsFlag lds_raised[2];  // one flag per kernel of this launcher
-    if constexpr (E::kActive) {
+    if constexpr (E::kGated) {
+        if (mr) return go(skinny_gated_kernel<LAYOUT, KS, NSS, RG, MAXM, true, YT>, &lds_raised[1]);
+        return go(skinny_gated_kernel<LAYOUT, KS, NSS, RG, MAXM, false, YT>, &lds_raised[0]);
+    } else if constexpr (E::kActive) {
         if (mr)
             return go(skinny_epilogue_kernel<LAYOUT, KS, NSS, RG, MAXM, true, YT>, &lds_raised[1]);
         return go(skinny_epilogue_kernel<LAYOUT, KS, NSS, RG, MAXM, false, YT>, &lds_raised[0]);
@@ -647,8 +696,13 @@ __device__ __forceinline__ void linear_decode_block(
     auto issue = [&](int64_t tile, int64_t u0, uint4 (&w)[RG][NSS], bool (&ok)[RG][NSS]) {
 #pragma unroll
         for (int q = 0; q < RG; ++q) {
-            const int64_t n = (tile * RG + q) * 16 + r;
+            int64_t n = (tile * RG + q) * 16 + r;
             const uint8_t *wrow = packed + n * rb;
+            if constexpr (E::kGated) {
+                const int64_t col = gated_col(n);
+                wrow = packed + (col + r / 8 * ep.F) * rb;
+                n = col < ep.F ? 0 : N;
+            }
 #pragma unroll
             for (int s = 0; s < NSS; ++s) {
                 const int64_t unit = u0 + (int64_t)(s * KS + wave) * 4 + g;
@@ -912,6 +966,15 @@ __global__ __launch_bounds__(64 * KS) void linear_decode_epilogue_kernel(
                                                                    nullptr, ep);
 }
 
+template <int LAYOUT, int KS, int NSS, int MAXM, bool STREAM, int RG, typename XT, typename YT>
+__global__ __launch_bounds__(64 * KS) void linear_decode_gated_kernel(
+    const XT *__restrict__ x, const uint8_t *__restrict__ packed,
+    const GammaMap gm, int M, int64_t N, int64_t K, int64_t rb,
+    YT *__restrict__ y, const GatedEpilogue<YT> ep) {
+    linear_decode_block<LAYOUT, KS, NSS, MAXM, STREAM, RG, XT, YT>(x, packed, gm, M, N, K, rb, y,
+                                                                   nullptr, ep);
+}
+
 template <int LAYOUT, int MAXM, int KS, int NSS, bool STREAM, typename XT, typename YT,
           int RG = 1, typename E>
 hipError_t launch_linear_m(const XT *x, const uint8_t *packed, const GammaMap &gamma, int64_t M,
@@ -922,7 +985,9 @@ hipError_t launch_linear_m(const XT *x, const uint8_t *packed, const GammaMap &g
     const size_t smem = (LAYOUT == kLayoutBase3 ? 8192 : 0) + (size_t)MAXM * (kRoundK + 16) +
                         2 * (size_t)RG * KS * 1024;
     auto kern = [] {
-        if constexpr (E::kActive)
+        if constexpr (E::kGated)
+            return linear_decode_gated_kernel<LAYOUT, KS, NSS, MAXM, STREAM, RG, XT, YT>;
+        else if constexpr (E::kActive)
             return linear_decode_epilogue_kernel<LAYOUT, KS, NSS, MAXM, STREAM, RG, XT, YT>;
         else
             return linear_decode_kernel<LAYOUT, KS, NSS, MAXM, STREAM, RG, XT, YT>;

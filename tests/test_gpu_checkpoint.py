@@ -1,0 +1,64 @@
+"""Activations kept in 8 bits: codes, scales and restored values bit for bit against
+the definition in fp32, over widths that groups and vectors do not divide."""
+import pytest
+import torch
+
+import gated_ref as gr
+from gated_ref import BF16, F32, TYPES
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bl():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from ternary_weight_linear_bitlinear_amd import bitlinear
+    return bitlinear
+
+
+def check(bl, x, out=F32):
+    kept = bl.bitlinear_checkpoint(x)
+    codes, scale = gr.quantised(x)
+    assert torch.equal(kept.scale.cpu(), scale)
+    assert torch.equal(kept.codes.cpu(), codes)
+    y = bl.bitlinear_checkpoint_restore(kept, out)
+    assert y.dtype is out and torch.equal(y.cpu(), gr.restored(codes, scale).to(out))
+    return kept
+
+
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (300, 5), (1, 8), (5, 9), (17, 63), (4, 64), (4, 65), (2, 127),
+                                 (333, 5001), (64, 2048), (9, 2056), (1000, 72), (31, 11008), (2, 70001), (1, 600001),
+                                 (5000, 66), (70000, 8)])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_bit_for_bit(bl, M, K, x):
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    v = torch.randn(M, K, generator=g, device="cuda") * torch.rand(M, 1, generator=g, device="cuda") * 30
+    check(bl, v.to(TYPES[x]), F32 if (M + K) % 2 else BF16)
+
+
+def test_ties_zeros_and_small_values(bl):
+    x = torch.zeros(4, 192, device="cuda")
+    x[0, :64] = torch.arange(64, device="cuda") - 31.5  # scale 32.5 in the middle group's place
+    x[0, 64:128] = (torch.arange(64, device="cuda") + 0.5) / 127 * 64
+    x[0, 64] = 64.0                                     # quotients at half codes
+    x[1, 3], x[1, 100] = 1e-7, -1e-9                    # below the least scale
+    x[2] = 1e30
+    check(bl, x)
+    check(bl, x.bfloat16(), BF16)
+
+
+def test_buffers_are_filled_and_nothing_else(bl):
+    M, K = 13, 1001
+    big = torch.full((M * K + 64,), 77, dtype=torch.int8, device="cuda")
+    scale = torch.full((M * gr.groups_of(K) + 16,), -1.0, device="cuda")
+    x = torch.randn(M, K, device="cuda")
+    kept = bl.Checkpoint(big[:M * K].view(M, K), scale[:M * gr.groups_of(K)].view(M, -1))
+    assert bl.bitlinear_checkpoint(x, kept) is kept
+    assert bool((big[M * K:] == 77).all()) and bool((scale[M * gr.groups_of(K):] == -1).all())
+    codes, s = gr.quantised(x)
+    assert torch.equal(kept.codes.cpu(), codes) and torch.equal(kept.scale.cpu(), s)
+
+
+def test_empty(bl):
+    kept = bl.bitlinear_checkpoint(torch.empty(0, 70, device="cuda"))
+    assert kept.scale.shape == (0, 2) and bl.bitlinear_checkpoint_restore(kept).shape == (0, 70)
