@@ -433,8 +433,8 @@ bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, cons
  *            segment: a plain matrix).
  *   grad_x   out [M, K] gx_dtype (fp32 sums, rounded once). The sums are rescaled by
  *            the ratio of two segments' gammas where one ends, one fp32 rounding each.
- * Any N and K (row counts that are multiples of 8 load faster). Dimensions above 2^24
- * return BL_ERR_INVALID_ARG. M = 0 is a no-op. */
+ * Any N and K (row counts that are multiples of 8 load faster). M or K above 2^24, or N
+ * above 2^23, return BL_ERR_INVALID_ARG. M = 0 is a no-op. */
 bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
                                              const uint8_t *packed, int layout,
                                              const float *gammas, const int64_t *seg_rows, int nseg,

@@ -543,7 +543,7 @@ bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
     bl::GammaMap gm;
     int64_t N = 0;
     if (!make_segments(gammas, seg_rows, nseg, gm, N)) return BL_ERR_INVALID_ARG;
-    if (M < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return BL_ERR_INVALID_ARG;
+    if (M < 0 || K < 1 || M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim) return BL_ERR_INVALID_ARG;
     if (!valid_dtype(gy_dtype) || !valid_dtype(gx_dtype) || !valid_layout(layout))
         return BL_ERR_INVALID_ARG;
     if (M == 0) return BL_OK;
