@@ -409,11 +409,20 @@ bl_status bitlinear_checkpoint(const void *x, int x_dtype, int64_t M, int64_t K,
 bl_status bitlinear_checkpoint_restore(const int8_t *codes, const float *scale, int64_t M, int64_t K,
                                        void *y, int y_dtype, void *stream);
 
+/* Device workspace (bytes) of bitlinear_backward_weight_codes and
+ * bitlinear_backward_input_segmented (N = sum(seg_rows)); 0 where none is needed, and
+ * for an empty or refused shape. With few output tiles several workgroups share one
+ * tile's sum and leave partial sums there, which are added in a fixed order. */
+size_t bitlinear_backward_weight_codes_workspace_bytes(int64_t M, int64_t N, int64_t K, int gw_dtype);
+size_t bitlinear_backward_input_segmented_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                                          int gy_dtype);
+
 /* bitlinear_backward_weight_codes: the weight gradient from the codes that the
  * forward product had, so that x itself need not be kept ([b158] §5.3 takes the
  * gradient with the dequantised x):
  *   grad_w[n, k] = sum_m (grad_y[m, n] * (scale[m] / 127)) * xq[m, k]
  *   grad_y   [M, N] gy_dtype; xq [M, K], scale [M]: from bitlinear_quant_acts.
+ *   workspace device scratch of at least the size above; NULL where that is 0.
  *   grad_w   out [N, K] gw_dtype. BL_F32: the factor in parentheses is rounded once
  *            to fp32 and enters as three exact bf16 pieces (for magnitudes >= 2^-110,
  *            as in bitlinear_backward_input), so products are exact and sums fp32;
@@ -423,7 +432,8 @@ bl_status bitlinear_checkpoint_restore(const int8_t *codes, const float *scale, 
  * BL_ERR_INVALID_ARG. N = 0 is a no-op; M = 0 writes zeros. */
 bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
                                           const float *scale, int64_t M, int64_t N, int64_t K,
-                                          void *grad_w, int gw_dtype, void *stream);
+                                          void *grad_w, int gw_dtype, void *workspace,
+                                          size_t workspace_bytes, void *stream);
 
 /* bitlinear_backward_input_segmented: the gradient of the input that a stack shares,
  *   grad_x[m, k] = sum_s gammas[s] * sum_{n in segment s} grad_y[m, n] * c[n, k]
@@ -431,6 +441,7 @@ bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, cons
  *            bitlinear_backward_input.
  *   packed, layout, gammas, seg_rows, nseg: as in bitlinear_forward_segmented (one
  *            segment: a plain matrix).
+ *   workspace as for bitlinear_backward_weight_codes.
  *   grad_x   out [M, K] gx_dtype (fp32 sums, rounded once). The sums are rescaled by
  *            the ratio of two segments' gammas where one ends, one fp32 rounding each.
  * Any N and K (row counts that are multiples of 8 load faster). M or K above 2^24, or N
@@ -439,7 +450,7 @@ bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
                                              const uint8_t *packed, int layout,
                                              const float *gammas, const int64_t *seg_rows, int nseg,
                                              int64_t M, int64_t K, void *grad_x, int gx_dtype,
-                                             void *stream);
+                                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---- Norms before and after a block ----------------------------------------
  *

@@ -144,10 +144,14 @@ _lib.bitlinear_checkpoint.argtypes = [_p, _int, _i64, _i64, _p, _p, _p]
 _lib.bitlinear_checkpoint_restore.restype = _int
 _lib.bitlinear_checkpoint_restore.argtypes = [_p, _p, _i64, _i64, _p, _int, _p]
 _lib.bitlinear_backward_weight_codes.restype = _int
-_lib.bitlinear_backward_weight_codes.argtypes = [_p, _int, _p, _p, _i64, _i64, _i64, _p, _int, _p]
+_lib.bitlinear_backward_weight_codes.argtypes = [_p, _int, _p, _p, _i64, _i64, _i64, _p, _int, _p, _sz, _p]
+_lib.bitlinear_backward_weight_codes_workspace_bytes.restype = _sz
+_lib.bitlinear_backward_weight_codes_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
+_lib.bitlinear_backward_input_segmented_workspace_bytes.restype = _sz
+_lib.bitlinear_backward_input_segmented_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
 _lib.bitlinear_backward_input_segmented.restype = _int
 _lib.bitlinear_backward_input_segmented.argtypes = [_p, _int, _p, _int, _p, _p, _int, _i64, _i64,
-                                                    _p, _int, _p]
+                                                    _p, _int, _p, _sz, _p]
 _lib.bitlinear_forward_plan.restype = _int
 _lib.bitlinear_forward_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, ctypes.c_char_p, _sz]
 _lib.bitlinear_status_string.restype = ctypes.c_char_p
@@ -166,7 +170,8 @@ EXPORTED = ["bitlinear_packed_row_bytes", "bitlinear_pack_workspace_bytes",
             "bitlinear_block_norm_backward", "bitlinear_forward_gated", "bitlinear_linear_gated",
             "bitlinear_gated_backward_workspace_bytes", "bitlinear_gated_backward",
             "bitlinear_checkpoint_groups", "bitlinear_checkpoint", "bitlinear_checkpoint_restore",
-            "bitlinear_backward_weight_codes", "bitlinear_backward_input_segmented",
+            "bitlinear_backward_weight_codes_workspace_bytes", "bitlinear_backward_weight_codes",
+            "bitlinear_backward_input_segmented_workspace_bytes", "bitlinear_backward_input_segmented",
             "bitlinear_forward_plan", "bitlinear_status_string",
             "bitlinear_version",
             "bitlinear_source_hash"]
@@ -1114,14 +1119,24 @@ def bitlinear_checkpoint_restore(kept: Checkpoint, out_dtype=None, y: torch.Tens
     return y
 
 
+@functools.lru_cache(maxsize=1024)
+def bitlinear_backward_weight_codes_workspace_bytes(M: int, N: int, K: int, out_dtype=torch.float32) -> int:
+    return int(_lib.bitlinear_backward_weight_codes_workspace_bytes(M, N, K, _code(out_dtype)))
+
+
+@functools.lru_cache(maxsize=1024)
+def bitlinear_backward_input_segmented_workspace_bytes(M: int, N: int, K: int, grad_dtype=torch.float32) -> int:
+    return int(_lib.bitlinear_backward_input_segmented_workspace_bytes(M, N, K, _code(grad_dtype)))
+
+
 def bitlinear_backward_weight_codes(grad_y: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,
                                     out_dtype=None, grad_w: torch.Tensor | None = None,
-                                    stream=None) -> torch.Tensor:
+                                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """grad_w [N, K] = sum_m grad_y[m, n] * (scale[m] / 127) * xq[m, k], from the codes
     that the forward product had (out_dtype: grad_w's type by default, then fp32)."""
     if stream is not None:
         with _on("bitlinear_backward_weight_codes", stream, grad_y):
-            return bitlinear_backward_weight_codes(grad_y, xq, scale, out_dtype, grad_w)
+            return bitlinear_backward_weight_codes(grad_y, xq, scale, out_dtype, grad_w, workspace)
     where = "bitlinear_backward_weight_codes"
     (M, N), dtype, dev, gy_at = _lead(where, "grad_y", grad_y)
     if xq.dim() != 2:
@@ -1130,21 +1145,25 @@ def bitlinear_backward_weight_codes(grad_y: torch.Tensor, xq: torch.Tensor, scal
     out_dtype = _out_dtype(where, out_dtype, grad_w)
     if grad_w is None:
         grad_w = torch.empty(N, K, dtype=out_dtype, device=grad_y.device)
+    need = bitlinear_backward_weight_codes_workspace_bytes(M, N, K, out_dtype)
+    hold, ws, ws_bytes = (None, None, 0) if need == 0 else _workspace(where, workspace, need, grad_y)
     _run(where, dev, _lib.bitlinear_backward_weight_codes,
          (gy_at, _code(dtype), _addr(where, "xq", xq, (M, K), torch.int8, dev),
           _addr(where, "scale", scale, (M,), _f32, dev), M, N, K,
-          _addr(where, "grad_w", grad_w, (N, K), out_dtype, dev), _code(out_dtype)))
+          _addr(where, "grad_w", grad_w, (N, K), out_dtype, dev), _code(out_dtype), ws, ws_bytes))
     return grad_w
 
 
 def bitlinear_backward_input_segmented(grad_y: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor,
                                        seg_rows, K: int, layout="2bit", out_dtype=None,
-                                       grad_x: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                                       grad_x: torch.Tensor | None = None,
+                                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """grad_x [M, K] of the input that a stack of matrices shares (seg_rows: N, or the
     row counts; gammas[s] each; out_dtype: grad_x's type by default, then fp32)."""
     if stream is not None:
         with _on("bitlinear_backward_input_segmented", stream, grad_y):
-            return bitlinear_backward_input_segmented(grad_y, packed, gammas, seg_rows, K, layout, out_dtype, grad_x)
+            return bitlinear_backward_input_segmented(grad_y, packed, gammas, seg_rows, K, layout, out_dtype, grad_x,
+                                                      workspace)
     where = "bitlinear_backward_input_segmented"
     lay = _one_of(where, "layout", layout, LAYOUTS)
     table, nseg, N = _segments(_rows_of(seg_rows))
@@ -1158,8 +1177,10 @@ def bitlinear_backward_input_segmented(grad_y: torch.Tensor, packed: torch.Tenso
     out_dtype = _out_dtype(where, out_dtype, grad_x)
     if grad_x is None:
         grad_x = torch.empty(M, K, dtype=out_dtype, device=grad_y.device)
+    need = bitlinear_backward_input_segmented_workspace_bytes(M, N, K, dtype)
+    hold, ws, ws_bytes = (None, None, 0) if need == 0 else _workspace(where, workspace, need, grad_y)
     _run(where, dev, _lib.bitlinear_backward_input_segmented,
          (gy_at, _code(dtype), _addr(where, "packed", packed, (N, _row_bytes(K, lay)), torch.uint8, dev), lay,
           gammas.data_ptr(), table, nseg, M, K, _addr(where, "grad_x", grad_x, (M, K), out_dtype, dev),
-          _code(out_dtype)))
+          _code(out_dtype), ws, ws_bytes))
     return grad_x

@@ -517,29 +517,47 @@ bl_status bitlinear_checkpoint_restore(const int8_t *codes, const float *scale, 
                                                   static_cast<hipStream_t>(stream)));
 }
 
+size_t bitlinear_backward_weight_codes_workspace_bytes(int64_t M, int64_t N, int64_t K, int gw_dtype) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim || !valid_dtype(gw_dtype))
+        return 0;
+    return bl::backward_weight_codes_workspace(M, N, K, gw_dtype);
+}
+
 bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
                                           const float *scale, int64_t M, int64_t N, int64_t K,
-                                          void *grad_w, int gw_dtype, void *stream) {
+                                          void *grad_w, int gw_dtype, void *workspace,
+                                          size_t workspace_bytes, void *stream) {
     if (M < 0 || N < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
         return BL_ERR_INVALID_ARG;
     if (!valid_dtype(gy_dtype) || !valid_dtype(gw_dtype)) return BL_ERR_INVALID_ARG;
-    if (!aligned16(grad_y) || !aligned16(xq) || !aligned16(scale) || !aligned16(grad_w))
+    if (!aligned16(grad_y) || !aligned16(xq) || !aligned16(scale) || !aligned16(grad_w) ||
+        !aligned16(workspace))
         return BL_ERR_INVALID_ARG;
     if (N == 0) return BL_OK;
     if (!grad_w || (M > 0 && (!grad_y || !xq || !scale))) return BL_ERR_INVALID_ARG;
+    const size_t need = bitlinear_backward_weight_codes_workspace_bytes(M, N, K, gw_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return BL_ERR_INVALID_ARG;
     bl_status st = device_ok();
     if (st != BL_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (M == 0) return launched(bl::launch_zero(grad_w, gw_dtype, N * K, s));
     return launched(bl::launch_backward_weight_codes(grad_y, gy_dtype, xq, scale, M, N, K, grad_w,
-                                                     gw_dtype, s));
+                                                     gw_dtype, static_cast<float *>(workspace), s));
+}
+
+size_t bitlinear_backward_input_segmented_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                                          int gy_dtype) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim ||
+        !valid_dtype(gy_dtype))
+        return 0;
+    return bl::backward_input_segmented_workspace(M, N, K, gy_dtype);
 }
 
 bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
                                              const uint8_t *packed, int layout,
                                              const float *gammas, const int64_t *seg_rows, int nseg,
                                              int64_t M, int64_t K, void *grad_x, int gx_dtype,
-                                             void *stream) {
+                                             void *workspace, size_t workspace_bytes, void *stream) {
     bl::GammaMap gm;
     int64_t N = 0;
     if (!make_segments(gammas, seg_rows, nseg, gm, N)) return BL_ERR_INVALID_ARG;
@@ -548,12 +566,16 @@ bl_status bitlinear_backward_input_segmented(const void *grad_y, int gy_dtype,
         return BL_ERR_INVALID_ARG;
     if (M == 0) return BL_OK;
     if (!grad_y || !packed || !gammas || !grad_x) return BL_ERR_INVALID_ARG;
-    if (!aligned16(grad_y) || !aligned16(packed) || !aligned4(gammas) || !aligned16(grad_x))
+    if (!aligned16(grad_y) || !aligned16(packed) || !aligned4(gammas) || !aligned16(grad_x) ||
+        !aligned16(workspace))
         return BL_ERR_INVALID_ARG;
+    const size_t need = bitlinear_backward_input_segmented_workspace_bytes(M, N, K, gy_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return BL_ERR_INVALID_ARG;
     bl_status st = device_ok();
     if (st != BL_OK) return st;
     return launched(bl::launch_backward_input_segmented(grad_y, gy_dtype, packed, layout, gm, M, N,
                                                         K, grad_x, gx_dtype,
+                                                        static_cast<float *>(workspace),
                                                         static_cast<hipStream_t>(stream)));
 }
 

@@ -11,10 +11,17 @@
 //           bf16.
 //   grad_x: i = m, j = k, p = n; A = grad_y as stored ([i][p]); B = packed codes,
 //           expanded to bf16.
-// An fp32 value of A is taken as three bf16 pieces (exact, f32_piece_bits), which are
-// multiplied by the same fragment of B one after the other: v is one fp32 rounding of
-// its product, each term of grad_w exact beyond it. grad_w in bf16 takes two pieces
-// (v to within 2^-15), far below its own rounding of 2^-8.
+// An fp32 value of A (v is one: one rounding of its product) enters in pieces that the
+// same fragment of B is multiplied by one after the other. Two ways:
+//   three bf16 pieces of 8 significant bits each: exact, whatever the values. grad_w in
+//   bf16 takes two of them (v to within 2^-15, far below its own rounding of 2^-8).
+//   two fp16 pieces of 11 bits, rounded to nearest: v to within 2^-22 of its magnitude
+//   (or 2^-39 of its column's largest, where that is more), for two thirds of the matrix-core work (one
+//   piece, 2^-11, for grad_w in bf16). fp16's range is short, so each row of C's values
+//   of A are scaled by a power of two that brings the largest to 2^14 .. 2^15, and the
+//   result back: a first kernel finds the largest.
+// Large tiles, bound by the matrix cores, take fp16; small ones, bound by latency, bf16
+// in one launch less.
 //
 // Each segment's sum has a factor of its own. Instead of a second set of sums the
 // running sums are rescaled where a segment ends, by the ratio of its gamma to the
@@ -29,6 +36,8 @@
 #include "bl_internal.hpp"
 #include "device_util.hpp"
 #include "row_share.hpp"
+
+#include <cmath>
 
 namespace bl {
 namespace {
@@ -45,7 +54,10 @@ struct CodesArgs {
     GammaMap gm;         // grad_x: the segments
     int64_t I, J, P;
     int tiles_i, tiles_j;
-    void *C;  // [I, J]
+    int splits;   // workgroups that share a tile's slices
+    const float *peak;  // fp16 pieces: the largest |A(i, .)|, [peaks, I]
+    int peaks;
+    void *C;      // [I, J]; with splits their partial sums, [splits, I, J] fp32
 };
 
 // Block tile BI x BJ outputs, contraction slice BP per stage, WI x WJ waves.
@@ -70,6 +82,19 @@ struct Stage {
     static_assert(SMEM <= (int)kLdsBytesPerCu, "two stages in LDS");
 };
 
+// LDS slot of 16-byte piece `c` of row `row` of B. A thread writes its codes' pieces
+// (two or four) one after the other, so that the lanes of one write stand 32 or 64
+// bytes apart and would meet on a quarter or a half of the banks; the pieces of a
+// thread are permuted so that lanes and neighbouring rows take different ones (input
+// gradient, 4096^3: a third of the LDS cycles were conflicts). Rows r and r + 4 have
+// the same order, so that a transposing load's lanes keep one offset.
+template <int BSRC>
+__device__ __forceinline__ int b_slot(int row, int c) {
+    if constexpr (BSRC == kBCodes8) return c ^ (c / 16 & 1);
+    const int u = c / 4;
+    return c ^ ((u + u / 4 + 3 * row) & 3);
+}
+
 // Eight elements from any address; those from `count` on are zero and not read.
 template <typename T>
 __device__ __forceinline__ void load8_some(const T *p, int64_t count, Raw8<T> &r) {
@@ -86,6 +111,39 @@ __device__ __forceinline__ void load8_some(const T *p, int64_t count, Raw8<T> &r
         r.a = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
+// Two values as two fp16 ones, rounded to nearest, in a word.
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ half2_t to_half2(float a, float b) {
+    return __builtin_convertvector(float2_t{a, b}, half2_t);
+}
+// The power of two that takes a row's largest value to 2^14 .. 2^15 (any, for rows of
+// values below 2^-112), and its inverse.
+__device__ __forceinline__ float peak_scale(float top) {
+    uint32_t e = __float_as_uint(top) >> 23;
+    e = e < 15u ? 15u : e;
+    return __uint_as_float((268u - e) << 23);
+}
+__device__ __forceinline__ float peak_inverse(float scale) {
+    return __uint_as_float((254u << 23) - __float_as_uint(scale));
+}
+
+// Memory of `bytes` bytes (as many as 32 bits hold) from a uniform address, as buffer
+// loads take it: offsets past it read zeros.
+typedef int v2i __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
+    const uint32_t n = bytes < 0xFFFFFFFFll ? (uint32_t)bytes : 0xFFFFFFFFu;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)n, 0x00020000);
+}
+__device__ __forceinline__ v4i load_v4(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
+}
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
 // x / 127, correctly rounded (Markstein's step from the rounded reciprocal).
 __device__ __forceinline__ float over127(float x) {
     constexpr float r = 1.0f / 127.0f;
@@ -101,7 +159,7 @@ __device__ __forceinline__ float over127(float x) {
 // the vector unit's work then runs in their shadow, and the registers are free for
 // the loads of the next stage at once. Fragments are read one group of
 // instructions ahead.
-template <typename T, bool A_T, int BSRC, int NP, bool VEC, typename GT, typename OT>
+template <typename T, bool A_T, int BSRC, int NP, bool HALF, bool VEC, typename GT, typename OT>
 __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs a) {
     using S = Stage<T, A_T, BSRC, NP>;
     constexpr int kT = T::kThreads;
@@ -110,9 +168,11 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     uint64_t *lut = reinterpret_cast<uint64_t *>(smem + 2 * S::BYTES);  // base-3 only
 
     const int ntiles = a.tiles_i * a.tiles_j;
-    const int per_xcd = (ntiles + kXcds - 1) / kXcds;
-    const int t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-    if (t >= ntiles) return;
+    const int per_xcd = (ntiles * a.splits + kXcds - 1) / kXcds;
+    int t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+    if (t >= ntiles * a.splits) return;
+    const int split = t / ntiles;
+    t -= split * ntiles;
     const int64_t i0 = (int64_t)(t / a.tiles_j) * T::BI;
     const int64_t j0 = (int64_t)(t % a.tiles_j) * T::BJ;
     const int tid = threadIdx.x;
@@ -122,7 +182,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     // Segments in the order of |gamma|: where they begin and end, and the factor
     // that the sums take before the segment's own terms.
     __shared__ int64_t seg_begin[kMaxSegments], seg_end[kMaxSegments];
-    __shared__ float seg_ratio[kMaxSegments + 1];
+    __shared__ float seg_ratio[kMaxSegments], seg_gamma[kMaxSegments];
     const int nseg = A_T ? 1 : a.gm.nseg;
     if constexpr (!A_T) {
         if (tid < nseg) {
@@ -139,7 +199,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
             seg_begin[rank] = tid == 0 ? 0 : a.gm.bound[tid - 1];
             seg_end[rank] = tid == nseg - 1 ? a.P : a.gm.bound[tid];
             seg_ratio[rank] = mine == 0.f ? 1.0f : before / mine;
-            if (rank == nseg - 1) seg_ratio[nseg] = mine;
+            seg_gamma[rank] = mine;
         }
         if constexpr (BSRC == kBPacked3) {
             for (int i = tid; i < 256; i += kT) lut[i] = base3_field_entry((uint32_t)i);
@@ -147,12 +207,16 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         __syncthreads();
     }
 
+    // fp16 pieces: scales of the thread's columns (A_T) or rows, inverses for the end
+    __shared__ float inverse[HALF ? T::BI : 1];
+
     // ---- global -> registers ------------------------------------------------------
     constexpr int A_ROW = A_T ? T::BI / 8 : T::BP / 8;  // chunks of eight in a tile row
     constexpr int A_CH = T::BI * T::BP / 8 / kT;
     static_assert(A_CH * 8 * kT == T::BI * T::BP && kT % A_ROW == 0, "whole chunks for every thread");
     constexpr int A_STEP = kT / A_ROW;  // tile rows between a thread's chunks
-    constexpr int B_EACH = BSRC == kBCodes8 ? 16 : 32, B_ROW = T::BJ / B_EACH;  // codes; threads of a row
+    // codes for each thread: 32 packed ones where that leaves none idle; threads of a row
+    constexpr int B_EACH = BSRC != kBCodes8 && T::BP * T::BJ / 32 >= kT ? 32 : 16, B_ROW = T::BJ / B_EACH;
     constexpr int B_CH = (T::BP * B_ROW + kT - 1) / kT;
     static_assert(T::BP * B_ROW % kT == 0 || T::BP * B_ROW < kT, "whole rows of B");
     constexpr int B_STEP = kT / B_ROW;
@@ -161,7 +225,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     v4i b_reg[B_CH];  // grad_w: 16 codes of one token; packed: as unpacked below
     const int ar = tid / A_ROW, ac = tid % A_ROW;
     const int br = tid / B_ROW, bc = tid % B_ROW;
-    const bool b_mine = B_CH > 1 || T::BP * B_ROW >= kT || br < T::BP;
+    const bool b_mine = T::BP * B_ROW >= kT || br < T::BP;
     const GT *const A = static_cast<const GT *>(a.A);
     const uint8_t *const B = static_cast<const uint8_t *>(a.B);
 
@@ -184,93 +248,174 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     }
     const int64_t c0 = j0 + (int64_t)B_EACH * bc;  // B's columns
     constexpr int kPer = BSRC == kBCodes8 ? 1 : BSRC == kBPacked2 ? 4 : BSRC == kBPacked1 ? 8 : 5;
-    // (packed rows are whole 16-byte pieces, so 2-bit and 1-bit pieces lie wholly in or
-    // past them; of base-3 the dwords past a row are taken from its start)
-    const int64_t b_first = BSRC == kBPacked3 ? c0 / 5 & ~(int64_t)3 : c0 / kPer;
-    constexpr int kWords = BSRC == kBPacked2 ? 2 : BSRC == kBPacked1 ? 1 : 3;
+    // (packed rows are whole 16-byte pieces; dwords past a row are taken from its start)
+    const int64_t b_first = c0 / kPer & ~(int64_t)3;
+    // the dwords that hold the codes (base-3 rows: from any byte on)
+    constexpr int kWords = BSRC == kBPacked2 ? B_EACH / 16 : BSRC == kBPacked1 ? 1 : B_EACH / 16 + 1;
     int b_at[3];  // bytes from the row's start; codes: the first only
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int64_t at = b_first + 4 * i;
         b_at[i] = BSRC == kBCodes8 ? (c0 < a.J ? (int)c0 : 0) : at < a.ldb ? (int)at : 0;
     }
-    const int b_shift = BSRC == kBPacked3 ? (int)(c0 / 5 - b_first) : 0;
+    const int b_shift = BSRC == kBPacked3 ? (int)(c0 / 5 - b_first) : BSRC == kBPacked1 ? (int)(c0 % 32 / 4) : 0;
     const int b_code = BSRC == kBPacked3 ? (int)(c0 % 5) : 0;
 
-    auto load_b = [&](int c, const uint8_t *row) __attribute__((always_inline)) {
-        if constexpr (BSRC == kBCodes8) {
-            b_reg[c] = VEC ? *reinterpret_cast<const v4i *>(row + b_at[0])
-                           : load16_any(reinterpret_cast<const int8_t *>(row) + b_at[0]);
-        } else if constexpr (BSRC == kBPacked2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(row + b_at[0]);
-            b_reg[c] = v4i{(int)v.x, (int)v.y, 0, 0};
-        } else {
-            uint32_t d[3] = {0u, 0u, 0u};
+    float a_pow[HALF ? (A_T ? 8 : A_CH) : 1];
+    if constexpr (HALF) {
+        // (the largest of each column over the runs: every thread takes a column's share)
+        constexpr int kShares = kT / T::BI;
+        static_assert(kShares >= 1 && kT % T::BI == 0, "a thread for each row of the tile");
+        float *red = reinterpret_cast<float *>(smem);  // [kShares][BI]
+        const int col = tid % T::BI, share = tid / T::BI;
+        const int64_t i = i0 + col < a.I ? i0 + col : a.I - 1;
+        float top = 0.f;
+#pragma unroll 8
+        for (int n = share; n < a.peaks; n += kShares) top = fmaxf(top, a.peak[n * a.I + i]);
+        red[tid] = top;
+        __syncthreads();
+        auto scale_of = [&](int row) {
+            float t = red[row];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) d[i] = *reinterpret_cast<const uint32_t *>(row + b_at[i]);
-            b_reg[c] = v4i{(int)d[0], (int)d[1], (int)d[2], 0};
+            for (int n = 1; n < kShares; ++n) t = fmaxf(t, red[n * T::BI + row]);
+            return peak_scale(t);
+        };
+#pragma unroll
+        for (int e = 0; e < (A_T ? 8 : A_CH); ++e) a_pow[e] = scale_of(A_T ? 8 * ac + e : ar + e * A_STEP);
+        if (tid < T::BI) inverse[tid] = peak_inverse(scale_of(tid));
+        __syncthreads();  // the memory is the stages' from here on
+    }
+
+    // Aligned rows load from buffers that end with the segment: what lies past it reads
+    // as zero (A needs that; a token's scale of zero does the same for its row), and no
+    // load has a branch or a select behind it. Of an [i][p] tile the columns past a
+    // segment's end are sent past the buffer's. (Unaligned fp32 rows of it load the
+    // same way, from a buffer that ends with the matrix; store_a clears their ends.)
+    const uint32_t b_row = (uint32_t)(br * a.ldb);
+    auto load_a_vec = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        const GT *at = A_T ? a_base[0] + p0 * a.lda : a_base[A_T ? 0 : c] + p0;
+        uint32_t off = a_off[A_T ? 0 : c];
+        if constexpr (A_T) off += (uint32_t)(c * A_STEP * a.lda * sizeof(GT));
+        else if constexpr (VEC) off = p0 + 8 * ac < p1 ? off : 0xFFFFFFFFu;
+        const auto buf = buffer_of(at, A_T ? ((p1 - p0) * a.lda - i0) * (int64_t)sizeof(GT)
+                                           : VEC ? 0xFFFFFFF0ll : (A + a.I * a.lda - at) * (int64_t)sizeof(GT));
+        const v4i q = load_v4(buf, off);
+        if constexpr (sizeof(GT) == 2) {
+            a_reg[c].a = __builtin_bit_cast(uint4, q);
+        } else {
+            a_reg[c].a = __builtin_bit_cast(float4, q);
+            a_reg[c].b = __builtin_bit_cast(float4, load_v4(buf, VEC && !A_T ? off | 16 : off + 16));
+        }
+        if constexpr (A_T)
+            a_scale[c] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                buffer_of(a.scale + p0, (p1 - p0) * 4), 4 * (ar + c * A_STEP), 0, 0));
+    };
+    auto load_b_vec = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        const auto buf = buffer_of(B + p0 * a.ldb, (p1 - p0) * a.ldb);
+        const uint32_t row = b_row + (uint32_t)(c * B_STEP * a.ldb);
+        if constexpr (BSRC == kBCodes8) {
+            b_reg[c] = load_v4(buf, row + b_at[0]);
+        } else if constexpr (BSRC == kBPacked2 && B_EACH == 32) {
+            const v2i v = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(buf, row + b_at[0], 0, 0));
+            b_reg[c] = v4i{v[0], v[1], 0, 0};
+        } else {
+            int d[3] = {0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                d[i] = __builtin_bit_cast(int, __builtin_amdgcn_raw_buffer_load_b32(buf, row + b_at[i], 0, 0));
+            b_reg[c] = v4i{d[0], d[1], d[2], 0};
         }
     };
-    // The slice [p0, p0 + BP) of a segment that ends at p1. A whole slice has no
-    // checks; unaligned pieces of [p][*] tiles at the right edge run on into the next
-    // rows, which have to be there.
-    auto load_stage = [&](int64_t p0, int64_t p1) __attribute__((always_inline)) {
-        const int64_t past = VEC || !A_T ? 0 : 16;  // rows that hold 16 elements, at least
-        if (p0 + T::BP + past <= p1) {
-#pragma unroll
-            for (int c = 0; c < A_CH; ++c) {
-                const GT *at = A_T ? a_base[0] + (p0 + c * A_STEP) * a.lda : a_base[A_T ? 0 : c] + p0;
-                const GT *src = reinterpret_cast<const GT *>(reinterpret_cast<const char *>(at) +
-                                                             a_off[A_T ? 0 : c]);
-                if constexpr (VEC) a_reg[c].load(src);
-                else load_any(src, a_reg[c]);
-                if constexpr (A_T) a_scale[c] = a.scale[p0 + ar + c * A_STEP];
+    // Other rows load unaligned pieces, which run on past a row's or a segment's end into
+    // what follows; where nothing does, at the end of the matrix, element by element. A
+    // row of 16 elements more is enough: 16 rows hold them at least.
+    auto load_a_any = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        const int row = ar + c * A_STEP;
+        if constexpr (A_T) {
+            const int64_t p = p0 + row < p1 ? p0 + row : p1 - 1;
+            a_scale[c] = p0 + row < p1 ? a.scale[p] : 0.f;
+            if (i0 + T::BI <= a.I || p0 + T::BP + 16 <= p1) {
+                load_any(a_base[0] + p * a.lda + (i0 + 8 * ac < a.I ? 8 * ac : 0), a_reg[c]);
+            } else {
+                const int64_t i = i0 + 8 * ac;
+                load8_some(A + p * a.lda + (i < a.I ? i : 0), i < a.I ? a.I - i : 0, a_reg[c]);
             }
-            if (b_mine) {
-#pragma unroll
-                for (int c = 0; c < B_CH; ++c) load_b(c, B + (p0 + br + c * B_STEP) * a.ldb);
-            }
-            return;
+        } else if (i0 + T::BI < a.I || p0 + T::BP <= a.lda) {
+            const GT *at = a_base[A_T ? 0 : c] + p0;
+            load_any(reinterpret_cast<const GT *>(reinterpret_cast<const char *>(at) + a_off[c]), a_reg[c]);
+        } else {
+            const int64_t i = i0 + row, p = p0 + 8 * ac;
+            const bool ok = i < a.I && p < p1;
+            load8_some(A + (ok ? i * a.lda + p : 0), ok ? p1 - p : 0, a_reg[c]);
         }
-        // the end of a segment: A is zero past it (B need not be)
-#pragma unroll
-        for (int c = 0; c < A_CH; ++c) {
-            const int row = ar + c * A_STEP;
-            const int64_t p = p0 + (A_T ? row : 8 * ac), i = i0 + (A_T ? 8 * ac : row);
-            const bool ok = p < p1 && i < a.I;
-            const int64_t left = !ok ? 0 : A_T ? a.I - i : p1 - p;
-            load8_some(A + (ok ? (A_T ? p * a.lda + i : i * a.lda + p) : 0), left, a_reg[c]);
-            if constexpr (A_T) a_scale[c] = a.scale[p < p1 ? p : p1 - 1];
-        }
-        if (!b_mine) return;
-#pragma unroll
-        for (int c = 0; c < B_CH; ++c) {
+    };
+    auto load_b_any = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        if constexpr (BSRC == kBCodes8) {
             const int64_t p = p0 + br + c * B_STEP;
             const uint8_t *row = B + (p < p1 ? p : p1 - 1) * a.ldb;
-            if constexpr (BSRC == kBCodes8) {
-                uint32_t d[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (c0 + e < a.J) d[e / 4] |= (uint32_t)row[c0 + e] << (8 * (e % 4));
-                b_reg[c] = v4i{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
-            } else {
-                load_b(c, row);
+            if (j0 + T::BJ <= a.J || p0 + T::BP + 16 <= p1) {
+                b_reg[c] = load16_any(reinterpret_cast<const int8_t *>(row) + b_at[0]);
+                return;
             }
+            uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c0 + e < a.J) d[e / 4] |= (uint32_t)row[c0 + e] << (8 * (e % 4));
+            b_reg[c] = v4i{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
+        } else {
+            load_b_vec(c, p0, p1);  // (packed rows are aligned whatever K is)
         }
+    };
+    auto load_a = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        if constexpr (VEC || (!A_T && sizeof(GT) == 4)) load_a_vec(c, p0, p1);
+        else load_a_any(c, p0, p1);
+    };
+    auto load_b = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
+        if constexpr (VEC) load_b_vec(c, p0, p1);
+        else if (b_mine) load_b_any(c, p0, p1);
     };
 
     // ---- registers -> LDS -----------------------------------------------------------
-    auto store_a = [&](uint8_t *st, int c) __attribute__((always_inline)) {
+    // (rest: contraction indexes from the slice's first to the segment's end)
+    auto store_a = [&](uint8_t *st, int c, int64_t rest) __attribute__((always_inline)) {
         uint8_t *dst = st + (ar + c * A_STEP) * S::LD_A + 16 * ac;
-        if constexpr (NP == 1) {
-            *reinterpret_cast<v4i *>(dst) = __builtin_bit_cast(v4i, a_reg[c].a);
+        const bool ends = !VEC && !A_T && rest < T::BP;  // uniform
+        if constexpr (NP == 1 && !HALF) {
+            v4i w = __builtin_bit_cast(v4i, a_reg[c].a);
+            if (ends) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] &= (8 * ac + 2 * e < rest ? 0xFFFF : 0) | (8 * ac + 2 * e + 1 < rest ? (int)0xFFFF0000u : 0);
+            }
+            *reinterpret_cast<v4i *>(dst) = w;
         } else {
             float v[8];
             a_reg[c].widen(v);
+            if (ends) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 8 * ac + e < rest ? v[e] : 0.f;
+            }
             if constexpr (A_T) {
                 const float f = over127(a_scale[c]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= f;
+            }
+            if constexpr (HALF) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= a_pow[A_T ? e : c];
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    v4i w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const half2_t h = to_half2(v[2 * e], v[2 * e + 1]);
+                        w[e] = __builtin_bit_cast(int, h);
+                        v[2 * e] -= (float)h[0];
+                        v[2 * e + 1] -= (float)h[1];
+                    }
+                    *reinterpret_cast<v4i *>(dst + n * S::PLANE) = w;
+                }
+                return;
             }
 #pragma unroll
             for (int n = 0; n < NP; ++n) {  // each piece of what the ones before leave
@@ -288,39 +433,48 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     };
     auto store_b = [&](uint8_t *st, int c) __attribute__((always_inline)) {
         if (!b_mine) return;
-        uint8_t *dst = st + NP * S::PLANE + (br + c * B_STEP) * S::LD_B + 2 * B_EACH * bc;
+        const int row = br + c * B_STEP;
+        uint8_t *dst = st + NP * S::PLANE + row * S::LD_B;
         uint32_t d[B_EACH / 2];
+        auto field = [](uint32_t f, uint32_t &d0, uint32_t &d1) {
+            if constexpr (HALF) field_to_half(f, d0, d1);
+            else field_to_bf16(f, d0, d1);
+        };
         if constexpr (BSRC == kBCodes8) {
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
                 const uint32_t w = (uint32_t)b_reg[c][e / 4];
                 const float lo = (float)(int8_t)(w >> (8 * (e % 4))), hi = (float)(int8_t)(w >> (8 * (e % 4 + 1)));
-                d[e / 2] = top_halves(__float_as_uint(lo), __float_as_uint(hi));
+                d[e / 2] = HALF ? __builtin_bit_cast(uint32_t, to_half2(lo, hi))
+                                : top_halves(__float_as_uint(lo), __float_as_uint(hi));
             }
         } else if constexpr (BSRC == kBPacked1) {
             // bit t of byte i is code 4 t + i; u = 2 bit picks -1 or +1
+            const uint32_t w = (uint32_t)b_reg[c][0] >> b_shift;
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-                field_to_bf16((((uint32_t)b_reg[c][0] >> t) & 0x01010101u) << 1, d[2 * t], d[2 * t + 1]);
+            for (int t = 0; t < B_EACH / 4; ++t) field(((w >> t) & 0x01010101u) << 1, d[2 * t], d[2 * t + 1]);
         } else if constexpr (BSRC == kBPacked3) {
-            // the eight bytes of codes c0 .. c0 + 31 lie in three dwords
-            uint32_t f[8];
-            base3_fields(__builtin_amdgcn_alignbyte(b_reg[c][1], b_reg[c][0], b_shift),
-                         __builtin_amdgcn_alignbyte(b_reg[c][2], b_reg[c][1], b_shift), b_code, lut, f);
+            // the four or eight bytes of the codes lie in one dword more
+            uint32_t f[B_EACH / 4];
+            const uint32_t lo = __builtin_amdgcn_alignbyte(b_reg[c][1], b_reg[c][0], b_shift);
+            if constexpr (B_EACH == 16)
+                base3_fields16(lo, b_code, lut, f);
+            else
+                base3_fields(lo, __builtin_amdgcn_alignbyte(b_reg[c][2], b_reg[c][1], b_shift), b_code, lut, f);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) field_to_bf16(f[w], d[2 * w], d[2 * w + 1]);
+            for (int w = 0; w < B_EACH / 4; ++w) field(f[w], d[2 * w], d[2 * w + 1]);
         } else {
             // field s of a word holds its codes 4 s .. 4 s + 3
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+            for (int w = 0; w < B_EACH / 16; ++w)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    field_to_bf16(((uint32_t)b_reg[c][w] >> (2 * s)) & 0x03030303u, d[8 * w + 2 * s],
+                    field(((uint32_t)b_reg[c][w] >> (2 * s)) & 0x03030303u, d[8 * w + 2 * s],
                                   d[8 * w + 2 * s + 1]);
         }
 #pragma unroll
         for (int q = 0; q < B_EACH / 8; ++q)
-            *reinterpret_cast<uint4 *>(dst + 16 * q) =
+            *reinterpret_cast<uint4 *>(dst + 16 * b_slot<BSRC>(row, B_EACH / 8 * bc + q)) =
                 make_uint4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
     };
 
@@ -335,14 +489,19 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     const int tr_row = 8 * (g16 / 2) + t16 / 4, tr_col = 2 * (16 * (g16 % 2) + 4 * (t16 % 4));
     const int a_lane = A_T ? tr_row * S::LD_A + tr_col + wi * (T::BI / T::WI) * 2
                            : (wi * (T::BI / T::WI) + lane % 32) * S::LD_A + 16 * (lane / 32);
-    const int b_lane = NP * S::PLANE + tr_row * S::LD_B + tr_col + wj * (T::BJ / T::WJ) * 2;
+    int b_lane[T::FJ];
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) {
+        const int col = tr_col + (wj * (T::BJ / T::WJ) + 32 * j) * 2;  // bytes
+        b_lane[j] = NP * S::PLANE + tr_row * S::LD_B + 16 * b_slot<BSRC>(tr_row, col / 16) + col % 16;
+    }
     auto a_frag = [&](const uint8_t *st, int ks, int n, int i) __attribute__((always_inline)) -> bf16x8 {
         const uint8_t *p = st + a_lane + n * S::PLANE;
         if constexpr (A_T) return tr_frag(p + 16 * ks * S::LD_A + i * 64, S::LD_A);
         else return *reinterpret_cast<const bf16x8 *>(p + i * 32 * S::LD_A + 32 * ks);
     };
     auto b_frag = [&](const uint8_t *st, int ks, int j) __attribute__((always_inline)) -> bf16x8 {
-        return tr_frag(st + b_lane + 16 * ks * S::LD_B + j * 64, S::LD_B);
+        return tr_frag(st + b_lane[j] + 16 * ks * S::LD_B, S::LD_B);
     };
     v16f acc[T::FI][T::FJ];
 #pragma unroll
@@ -357,64 +516,94 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         int seg;
         int64_t p, end;
     };
-    auto begin_of = [&](int s) { return A_T ? (int64_t)0 : seg_begin[s]; };
-    auto end_of = [&](int s) { return A_T ? a.P : seg_end[s]; };
-    auto after = [&](Slice s) {  // seg == nseg: none
-        s.p += T::BP;
-        if (s.p >= s.end && ++s.seg < nseg) s.p = begin_of(s.seg), s.end = end_of(s.seg);
+    auto begin_of = [&](int s) { return A_T ? (int64_t)0 : uniform(seg_begin[s]); };
+    auto end_of = [&](int s) { return A_T ? a.P : uniform(seg_end[s]); };
+    auto after = [&](Slice s) {  // the last one again past the end
+        if (s.p + T::BP < s.end) {
+            s.p += T::BP;
+        } else if (s.seg + 1 < nseg) {
+            ++s.seg;
+            s.p = begin_of(s.seg), s.end = end_of(s.seg);
+        }
         return s;
     };
+    // this workgroup's share of them: `left` slices from cur on
+    int64_t slices = 0;
+    for (int s = 0; s < nseg; ++s) slices += (end_of(s) - begin_of(s) + T::BP - 1) / T::BP;
+    int64_t skip = slices * split / a.splits, left = slices * (split + 1) / a.splits - skip;
     Slice cur{0, begin_of(0), end_of(0)};
-    load_stage(cur.p, cur.end);
+    for (int64_t n; skip >= (n = (cur.end - cur.p + T::BP - 1) / T::BP);) {
+        skip -= n;
+        ++cur.seg;
+        cur.p = begin_of(cur.seg);
+        cur.end = end_of(cur.seg);
+    }
+    cur.p += skip * T::BP;
+    // Registers hold the next slice, LDS the current one. A piece's register is loaded
+    // again as soon as it has been converted, so that every load has a whole stage's
+    // time; past the last slice it is loaded and converted again, and never multiplied.
+    // (Unaligned rows, whose ends may load element by element, leave that out.)
+    constexpr int kTasks = A_CH + B_CH;
+    auto task = [&](int q, uint8_t *to, const Slice &held, const Slice &s, bool real) __attribute__((always_inline)) {
+        if (q < A_CH) {
+            store_a(to, q, held.end - held.p);
+            if (VEC || real) load_a(q, s.p, s.end);
+        } else {
+            store_b(to, q - A_CH);
+            if (VEC || real) load_b(q - A_CH, s.p, s.end);
+        }
+    };
 #pragma unroll
-    for (int c = 0; c < A_CH; ++c) store_a(smem, c);
+    for (int c = 0; c < A_CH; ++c) load_a(c, cur.p, cur.end);
 #pragma unroll
-    for (int c = 0; c < B_CH; ++c) store_b(smem, c);
+    for (int c = 0; c < B_CH; ++c) load_b(c, cur.p, cur.end);
     Slice next = after(cur);
-    if (next.seg < nseg) load_stage(next.p, next.end);
+#pragma unroll
+    for (int q = 0; q < kTasks; ++q) task(q, smem, cur, next, left > 1);
     __syncthreads();
+    // A stage's groups of instructions: one piece of A and one k-step each, their
+    // fragments read a group ahead.
     constexpr int kGroups = T::KSTEPS * NP;
+    bf16x8 af[2][T::FI], bb[2][T::FJ];
+    auto read_frags = [&](const uint8_t *st, int g) __attribute__((always_inline)) {
+        const int ks = g / NP, n = g % NP;
+        if (n == 0) {
+#pragma unroll
+            for (int j = 0; j < T::FJ; ++j) bb[ks & 1][j] = b_frag(st, ks, j);
+        }
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i) af[g & 1][i] = a_frag(st, ks, n, i);
+    };
+    auto multiply = [&](int g) __attribute__((always_inline)) {
+        const int ks = g / NP;
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FJ; ++j) {
+                if constexpr (HALF)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(half8_t, af[g & 1][i]), __builtin_bit_cast(half8_t, bb[ks & 1][j]),
+                        acc[i][j], 0, 0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[g & 1][i], bb[ks & 1][j],
+                                                                        acc[i][j], 0, 0, 0);
+            }
+    };
     for (int buf = 0;; buf ^= 1) {
         const uint8_t *st = smem + buf * S::BYTES;
         uint8_t *to = smem + (buf ^ 1) * S::BYTES;
-        const bool more = next.seg < nseg;
-        const Slice then = more ? after(next) : next;
-        bf16x8 af[2][T::FI], bb[2][T::FJ];
-#pragma unroll
-        for (int j = 0; j < T::FJ; ++j) bb[0][j] = b_frag(st, 0, j);
-#pragma unroll
-        for (int i = 0; i < T::FI; ++i) af[0][i] = a_frag(st, 0, 0, i);
+        const Slice then = after(next);
+        read_frags(st, 0);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int ks = g / NP;
-            if (g + 1 < kGroups) {
-                const int k1 = (g + 1) / NP, n1 = (g + 1) % NP;
-                if (n1 == 0) {
-#pragma unroll
-                    for (int j = 0; j < T::FJ; ++j) bb[k1 & 1][j] = b_frag(st, k1, j);
-                }
-#pragma unroll
-                for (int i = 0; i < T::FI; ++i) af[(g + 1) & 1][i] = a_frag(st, k1, n1, i);
-            }
+            if (g + 1 < kGroups) read_frags(st, g + 1);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-                for (int j = 0; j < T::FJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[g & 1][i], bb[ks & 1][j], acc[i][j],
-                                                                        0, 0, 0);
+            multiply(g);
             // this group's share of the next stage
-            if (more) {
-                constexpr int kTasks = A_CH + B_CH;
 #pragma unroll
-                for (int q = g * kTasks / (kGroups - 1); q < (g + 1) * kTasks / (kGroups - 1); ++q) {
-                    if (q < A_CH) store_a(to, q);
-                    else if (q < kTasks) store_b(to, q - A_CH);
-                }
-                if (g == kGroups - 1 && then.seg < nseg) load_stage(then.p, then.end);
-            }
+            for (int q = g * kTasks / kGroups; q < (g + 1) * kTasks / kGroups; ++q) task(q, to, next, then, left > 2);
         }
-        if (!more) break;
+        if (left == 1) break;
         if (next.seg != cur.seg) {
             const float f = seg_ratio[next.seg];
 #pragma unroll
@@ -426,13 +615,14 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         }
         cur = next;
         next = then;
+        --left;
         lds_barrier();
     }
 
     // ---- epilogue: lane holds D[i][j] for j = lane % 32 and
     // i = 8 (r / 4) + 4 (lane / 32) + r % 4, register r
-    const float alpha = A_T ? 1.0f : seg_ratio[nseg];
-    OT *C = static_cast<OT *>(a.C);
+    const float alpha = A_T ? 1.0f : seg_gamma[cur.seg];
+    OT *C = static_cast<OT *>(a.C) + split * a.I * a.J;
 #pragma unroll
     for (int fi = 0; fi < T::FI; ++fi)
 #pragma unroll
@@ -440,19 +630,164 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
             const int64_t j = j0 + wj * (T::BJ / T::WJ) + fj * 32 + lane % 32;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int64_t i =
-                    i0 + wi * (T::BI / T::WI) + fi * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-                if (i < a.I && j < a.J) put(C, i * a.J + j, A_T ? acc[fi][fj][r] : acc[fi][fj][r] * alpha);
+                const int row = wi * (T::BI / T::WI) + fi * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+                float v = acc[fi][fj][r];
+                if constexpr (!A_T) v *= alpha;
+                if constexpr (HALF) v *= inverse[row];
+                if (i0 + row < a.I && j < a.J) put(C, (i0 + row) * a.J + j, v);
             }
         }
 }
 
-template <typename T, bool A_T, int BSRC, int NP, typename GT, typename OT>
+// The largest |v| of each column of grad_y [M, N] over a run of tokens: eight columns
+// and every eighth token of the run for each thread.
+template <typename GT, bool VEC>
+__global__ __launch_bounds__(256) void codes_peak_cols_kernel(const GT *grad_y, const float *scale, int64_t M,
+                                                              int64_t N, float *peak) {
+    __shared__ float red[8][256];
+    const int r = threadIdx.x / 32;
+    const int64_t n0 = (int64_t)blockIdx.x * 256;
+    const int left = (int)(N - n0 < 256 ? N - n0 : 256);
+    const Share<1, VEC> sh{left, (int)threadIdx.x % 32, 32};
+    const int64_t m0 = M * blockIdx.y / gridDim.y, m1 = M * (blockIdx.y + 1) / gridDim.y;
+    float top[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t m = m0 + r; m < m1; m += 32) {
+        RowRegs<GT, 1, VEC> g[4];
+        float f[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // (tokens past the run read its last one)
+            const int64_t mu = m + 8 * u < m1 ? m + 8 * u : m1 - 1;
+            g[u].load(grad_y + mu * N + n0, sh);
+            f[u] = over127(scale[mu]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float v[8];
+            g[u].widen(0, sh, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], fabsf(v[e] * f[u]));
+        }
+    }
+    const int start = sh.start(0), skip = sh.skip(0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e >= skip) red[r][start + e] = top[e];
+    __syncthreads();
+    if ((int)threadIdx.x >= left) return;
+    float t = red[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = fmaxf(t, red[i][threadIdx.x]);
+    peak[blockIdx.y * N + n0 + threadIdx.x] = t;
+}
+// The largest |grad_y| of each row (fp32).
+__global__ __launch_bounds__(256) void codes_peak_rows_kernel(const float *grad_y, int64_t N, float *peak) {
+    __shared__ float red[4];
+    const float *row = grad_y + (int64_t)blockIdx.x * N;
+    float top = 0.f;
+    if (N % 4 == 0) {
+        for (int64_t n = (int64_t)threadIdx.x * 4; n < N; n += 1024) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + n);
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+        }
+    } else {
+        for (int64_t n = threadIdx.x; n < N; n += 256) top = fmaxf(top, fabsf(row[n]));
+    }
+    top = wave_max0_dpp(top);
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) peak[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// out = the sum of `splits` partial results, in order.
+template <typename OT>
+__global__ __launch_bounds__(256) void codes_sum_kernel(const float *__restrict__ part, OT *__restrict__ out,
+                                                        int64_t count, int splits) {
+    const int64_t stride = (int64_t)gridDim.x * 256 * 4;
+    int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (count % 4 == 0) {
+        for (; at < count; at += stride) {
+            float4 s = *reinterpret_cast<const float4 *>(part + at);
+            for (int n = 1; n < splits; ++n) {
+                const float4 q = *reinterpret_cast<const float4 *>(part + n * count + at);
+                s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+            }
+            if constexpr (sizeof(OT) == 4) {
+                *reinterpret_cast<float4 *>(out + at) = s;
+            } else {
+                const bf16x2 lo = {(__bf16)s.x, (__bf16)s.y}, hi = {(__bf16)s.z, (__bf16)s.w};
+                *reinterpret_cast<uint2 *>(out + at) =
+                    make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+            }
+        }
+        return;
+    }
+    for (; at < count; at += stride) {
+        for (int64_t i = at; i < at + 4 && i < count; ++i) {
+            float s = part[i];
+            for (int n = 1; n < splits; ++n) s += part[n * count + i];
+            put(out, i, s);
+        }
+    }
+}
+
+// How A enters: as stored (bf16 grad_y), or the pieces of fp32 values in each tile size.
+enum CodesKind { kStored, kWeight32, kWeight16, kInput32 };  // kWeight16: grad_w in bf16
+template <int KIND>
+struct KindOf {
+    static constexpr bool kHalf = KIND != kStored;                       // in large tiles
+    static constexpr int kLarge = KIND == kStored || KIND == kWeight16 ? 1 : 2;
+    static constexpr int kSmall = KIND == kStored ? 1 : KIND == kWeight16 ? 2 : 3;
+};
+
+// How a product runs: 256 x 256 tiles or 64 x 64 ones, and the workgroups that share
+// a tile's slices where there are few tiles: whichever takes the least time by a model
+// of what was measured (64 contraction indexes in us; fixed costs in them too).
+//   large tiles: a round of one for each compute unit, `large` us;
+//   small tiles: `small` us alone, `full` for each where they fill the card, up to
+//   three (two) of them side by side;
+//   partial sums: written and read at 5 TB/s, and a launch more; the search for the
+//   largest values of fp16 pieces: a launch, and A read at 3 TB/s.
+struct CodesPlan {
+    bool large;
+    int splits;
+};
+CodesPlan codes_plan(int64_t I, int64_t J, int64_t P, int kind) {
+    static const struct { double large, small, full; int side; } kCost[4] = {
+        {1.6, 0.47, 0.28, 3}, {2.9, 1.5, 0.8, 3}, {1.95, 0.97, 0.55, 2}, {2.75, 0.8, 0.55, 2}};
+    const auto &c = kCost[kind];
+    const double slices = (double)((P + 63) / 64), out = (double)I * (double)J;
+    const double peaks = kind == kStored ? 0.0 : 6.0 + (double)I * (double)P * (kind == kInput32 ? 4e-6 : 2e-6) / 3;
+    auto tiles = [&](int64_t side) { return (double)((I + side - 1) / side) * (double)((J + side - 1) / side); };
+    CodesPlan best{true, 1};
+    double least = 1e30;
+    for (int n = 1; n <= 16 && n <= slices; ++n) {
+        const double share = std::ceil(slices / n), sums = n > 1 ? 5.0 + out * 8e-6 / 5 * n : 0.0;
+        const double large = std::ceil(tiles(256) * n / 256) * (share + 2.5) * c.large + peaks + sums;
+        const double alone = std::ceil(tiles(64) * n / (256 * c.side)) * (share + 1.5) * c.small;
+        const double small = std::fmax(alone, tiles(64) * slices * c.full / 256) + sums;
+        if (large < least) least = large, best = {true, n};
+        if (small < least) least = small, best = {false, n};
+    }
+    return best;
+}
+constexpr int64_t kPeakRuns = 64;  // of at least 32 tokens, which a workgroup loads at once
+int64_t peak_runs(int64_t M) { return M < 32 * kPeakRuns ? (M + 31) / 32 : kPeakRuns; }
+// Floats of partial sums, and of the largest values behind them.
+int64_t codes_partials(const CodesPlan &p, int64_t I, int64_t J) {
+    return p.splits > 1 ? ((int64_t)p.splits * I * J + 3) / 4 * 4 : 0;
+}
+size_t codes_workspace(int64_t I, int64_t J, int64_t P, int kind) {
+    const CodesPlan p = codes_plan(I, J, P, kind);
+    const int64_t peaks = !p.large || kind == kStored ? 0 : kind == kInput32 ? I : peak_runs(P) * I;
+    return (size_t)(codes_partials(p, I, J) + peaks) * sizeof(float);
+}
+
+template <typename T, bool A_T, int BSRC, int NP, bool HALF, typename GT, typename OT>
 hipError_t launch_codes(CodesArgs a, bool vec, hipStream_t s) {
     using S = Stage<T, A_T, BSRC, NP>;
     a.tiles_i = (int)((a.I + T::BI - 1) / T::BI);
     a.tiles_j = (int)((a.J + T::BJ - 1) / T::BJ);
-    const int64_t blocks = ((int64_t)a.tiles_i * a.tiles_j + kXcds - 1) / kXcds * kXcds;
+    const int64_t blocks = ((int64_t)a.tiles_i * a.tiles_j * a.splits + kXcds - 1) / kXcds * kXcds;
     auto go = [&](auto kern, LdsFlag *flag) {
         hipError_t e = allow_dynamic_lds(kern, S::SMEM, flag);
         if (e != hipSuccess) return e;
@@ -460,45 +795,100 @@ hipError_t launch_codes(CodesArgs a, bool vec, hipStream_t s) {
         return hipGetLastError();
     };
     static LdsFlag lds_raised[2];
-    if (vec) return go(codes_gemm_kernel<T, A_T, BSRC, NP, true, GT, OT>, &lds_raised[1]);
-    return go(codes_gemm_kernel<T, A_T, BSRC, NP, false, GT, OT>, &lds_raised[0]);
+    if (vec) return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, true, GT, OT>, &lds_raised[1]);
+    return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, false, GT, OT>, &lds_raised[0]);
 }
 
-template <bool A_T, int BSRC, int NP, typename GT, typename OT>
-hipError_t launch_codes_sized(const CodesArgs &a, bool vec, hipStream_t s) {
-    constexpr int BP = NP == 1 ? 64 : 32;
-    auto tiles = [&](int64_t bi, int64_t bj) { return ((a.I + bi - 1) / bi) * ((a.J + bj - 1) / bj); };
-    if (tiles(256, 256) >= 256) return launch_codes<Tile<256, 256, BP, 2, 4>, A_T, BSRC, NP, GT, OT>(a, vec, s);
-    if (tiles(128, 256) >= 128) return launch_codes<Tile<128, 256, BP, 2, 4>, A_T, BSRC, NP, GT, OT>(a, vec, s);
-    return launch_codes<Tile<64, 64, 64, 2, 2>, A_T, BSRC, NP, GT, OT>(a, vec, s);
+// The largest |A(i, .)| in a.peak.
+template <bool A_T, typename GT>
+hipError_t launch_peaks(const CodesArgs &a, float *peak, hipStream_t s) {
+    if constexpr (A_T) {
+        const GT *g = static_cast<const GT *>(a.A);
+        const dim3 grid((unsigned)((a.I + 255) / 256), (unsigned)a.peaks);
+        if (a.I % 8 == 0)
+            hipLaunchKernelGGL((codes_peak_cols_kernel<GT, true>), grid, dim3(256), 0, s, g, a.scale, a.P, a.I, peak);
+        else
+            hipLaunchKernelGGL((codes_peak_cols_kernel<GT, false>), grid, dim3(256), 0, s, g, a.scale, a.P, a.I, peak);
+    } else {
+        hipLaunchKernelGGL(codes_peak_rows_kernel, dim3((unsigned)a.I), dim3(256), 0, s,
+                           static_cast<const float *>(a.A), a.P, peak);
+    }
+    return hipGetLastError();
+}
+
+template <int KIND, int BSRC, typename GT, typename OT>
+hipError_t launch_codes_kind(CodesArgs a, bool vec, float *workspace, hipStream_t s) {
+    using K = KindOf<KIND>;
+    constexpr bool A_T = KIND == kWeight32 || KIND == kWeight16;
+    using Large = Tile<256, 256, KIND == kStored ? 64 : 32, 2, 4>;
+    // (a stage of three pieces of a [p][i] tile of 64 would leave one workgroup to a
+    // compute unit: 1024 tiles 1.1 us each and none side by side)
+    using Small = Tile<64, 64, KIND == kWeight32 ? 32 : 64, 2, 2>;
+    const CodesPlan plan = codes_plan(a.I, a.J, a.P, KIND);
+    a.splits = plan.splits;
+    if constexpr (K::kHalf) {
+        if (plan.large) {
+            float *peak = workspace + codes_partials(plan, a.I, a.J);
+            a.peaks = A_T ? (int)peak_runs(a.P) : 1;
+            a.peak = peak;
+            const hipError_t e = launch_peaks<A_T, GT>(a, peak, s);
+            if (e != hipSuccess) return e;
+        }
+    }
+    OT *out = static_cast<OT *>(a.C);
+    auto go = [&](auto *type) {
+        using T = Pointee<decltype(type)>;
+        return plan.large ? launch_codes<Large, A_T, BSRC, K::kLarge, K::kHalf, GT, T>(a, vec, s)
+                          : launch_codes<Small, A_T, BSRC, K::kSmall, false, GT, T>(a, vec, s);
+    };
+    if (plan.splits == 1) return go(out);
+    a.C = workspace;
+    const hipError_t e = go(workspace);
+    if (e != hipSuccess) return e;
+    const int64_t count = a.I * a.J, want = (count + 1023) / 1024;
+    hipLaunchKernelGGL(codes_sum_kernel<OT>, dim3((unsigned)(want < 8192 ? want : 8192)), dim3(256), 0, s,
+                       workspace, out, count, plan.splits);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+size_t backward_weight_codes_workspace(int64_t M, int64_t N, int64_t K, int gw_dtype) {
+    return codes_workspace(N, K, M, gw_dtype == kF32 ? kWeight32 : kWeight16);
+}
+size_t backward_input_segmented_workspace(int64_t M, int64_t N, int64_t K, int gy_dtype) {
+    return codes_workspace(M, K, N, gy_dtype == kF32 ? kInput32 : kStored);
+}
+
 hipError_t launch_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
                                         const float *scale, int64_t M, int64_t N, int64_t K,
-                                        void *grad_w, int gw_dtype, hipStream_t stream) {
-    CodesArgs a{grad_y, N, xq, K, scale, {}, N, K, M, 0, 0, grad_w};
+                                        void *grad_w, int gw_dtype, float *workspace,
+                                        hipStream_t stream) {
+    const CodesArgs a{grad_y, N, xq, K, scale, {}, N, K, M, 0, 0, 1, nullptr, 0, grad_w};
     const bool vec = N % 8 == 0 && K % 16 == 0;
     return typed(gy_dtype, [&](auto g) {
         using GT = Pointee<decltype(g)>;
-        if (gw_dtype == kF32) return launch_codes_sized<true, kBCodes8, 3, GT, float>(a, vec, stream);
-        return launch_codes_sized<true, kBCodes8, 2, GT, uint16_t>(a, vec, stream);
+        if (gw_dtype == kF32)
+            return launch_codes_kind<kWeight32, kBCodes8, GT, float>(a, vec, workspace, stream);
+        return launch_codes_kind<kWeight16, kBCodes8, GT, uint16_t>(a, vec, workspace, stream);
     });
 }
 
 hipError_t launch_backward_input_segmented(const void *grad_y, int gy_dtype, const uint8_t *packed,
                                            int layout, const GammaMap &gamma, int64_t M, int64_t N,
-                                           int64_t K, void *grad_x, int gx_dtype, hipStream_t stream) {
-    const CodesArgs a{grad_y, N, packed, row_bytes_of(layout, K), nullptr, gamma, M, K, N, 0, 0, grad_x};
+                                           int64_t K, void *grad_x, int gx_dtype, float *workspace,
+                                           hipStream_t stream) {
+    const CodesArgs a{grad_y, N, packed, row_bytes_of(layout, K), nullptr, gamma, M, K, N,
+                      0, 0, 1, nullptr, 0, grad_x};
     bool vec = N % 8 == 0;
     for (int s = 0; s + 1 < gamma.nseg; ++s) vec = vec && gamma.bound[s] % 8 == 0;
     auto go = [&](auto src_c) {
         constexpr int B = decltype(src_c)::value;
         return typed(gx_dtype, [&](auto o) {
             using OT = Pointee<decltype(o)>;
-            if (gy_dtype == kF32) return launch_codes_sized<false, B, 3, float, OT>(a, vec, stream);
-            return launch_codes_sized<false, B, 1, uint16_t, OT>(a, vec, stream);
+            if (gy_dtype == kF32)
+                return launch_codes_kind<kInput32, B, float, OT>(a, vec, workspace, stream);
+            return launch_codes_kind<kStored, B, uint16_t, OT>(a, vec, workspace, stream);
         });
     };
     switch (layout) {

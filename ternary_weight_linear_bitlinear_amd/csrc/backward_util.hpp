@@ -16,14 +16,20 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 // Four codes of one 2-bit field (bytes u = c + 1 in 0..2) to four bf16 values
 // -1 / 0 / +1 (0xBF80 / 0x0000 / 0x3F80) in two dwords. The byte permute picks
 // table bytes by selector: selector (u, u + 4) yields (low byte, high byte).
-__device__ __forceinline__ void field_to_bf16(uint32_t f, uint32_t &d0, uint32_t &d1) {
-    constexpr uint32_t kLo = 0x00800080u;  // u = 0, 1, 2 -> 0x80, 0x00, 0x80
-    constexpr uint32_t kHi = 0x003F00BFu;  // u = 0, 1, 2 -> 0xBF, 0x00, 0x3F
+template <uint32_t kLo, uint32_t kHi>
+__device__ __forceinline__ void field_to_16(uint32_t f, uint32_t &d0, uint32_t &d1) {
     const uint32_t f4 = f + 0x04040404u;
     const uint32_t s0 = __builtin_amdgcn_perm(f4, f, 0x05010400u);  // u0, u0+4, u1, u1+4
     const uint32_t s1 = __builtin_amdgcn_perm(f4, f, 0x07030602u);  // u2, u2+4, u3, u3+4
     d0 = __builtin_amdgcn_perm(kHi, kLo, s0);
     d1 = __builtin_amdgcn_perm(kHi, kLo, s1);
+}
+__device__ __forceinline__ void field_to_bf16(uint32_t f, uint32_t &d0, uint32_t &d1) {
+    // u = 0, 1, 2 -> low byte 0x80, 0x00, 0x80, high byte 0xBF, 0x00, 0x3F
+    field_to_16<0x00800080u, 0x003F00BFu>(f, d0, d1);
+}
+__device__ __forceinline__ void field_to_half(uint32_t f, uint32_t &d0, uint32_t &d1) {
+    field_to_16<0u, 0x003C00BCu>(f, d0, d1);  // -1 / 0 / +1 are 0xBC00 / 0x0000 / 0x3C00
 }
 
 // Base-3 decode table entry for byte v: its five trits t_r = c_r + 1 (first
@@ -65,6 +71,20 @@ __device__ __forceinline__ void base3_fields(uint32_t w0, uint32_t w1, int first
         out[2 * w] = (uint32_t)v;
         out[2 * w + 1] = (uint32_t)(v >> 32);
     }
+}
+
+// The same for 16 codes: four bytes hold the 16 fields from field `first` on.
+__device__ __forceinline__ void base3_fields16(uint32_t w, int first, const uint64_t *lut,
+                                               uint32_t (&out)[4]) {
+    const uint64_t e0 = lut[w & 0xFFu], e1 = lut[(w >> 8) & 0xFFu], e2 = lut[(w >> 16) & 0xFFu],
+                   e3 = lut[w >> 24];
+    // bytes 0..4 of each entry, one after the other: five words
+    const uint32_t f[5] = {(uint32_t)e0, (uint32_t)(e0 >> 32) | (uint32_t)e1 << 8,
+                           (uint32_t)(e1 >> 24) | (uint32_t)e2 << 16,
+                           (uint32_t)(e2 >> 16) | (uint32_t)e3 << 24, (uint32_t)(e3 >> 8)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = first == 4 ? f[i + 1] : __builtin_amdgcn_alignbyte(f[i + 1], f[i], first);
 }
 
 // The top halves of two fp32 words as one word of two bf16 values.

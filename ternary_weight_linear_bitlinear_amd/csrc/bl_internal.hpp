@@ -310,11 +310,15 @@ hipError_t launch_backward_weight(const void *grad_y, const void *x, bool f32, i
 // grad_w [N, K] = sum_m grad_y[m, n] * (scale[m] / 127) * xq[m, k].
 hipError_t launch_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
                                         const float *scale, int64_t M, int64_t N, int64_t K,
-                                        void *grad_w, int gw_dtype, hipStream_t stream);
+                                        void *grad_w, int gw_dtype, float *workspace,
+                                        hipStream_t stream);
+size_t backward_weight_codes_workspace(int64_t M, int64_t N, int64_t K, int gw_dtype);  // bytes
 // grad_x [M, K] = sum over segments of gamma_s * grad_y_s [M, rows_s] . codes_s.
 hipError_t launch_backward_input_segmented(const void *grad_y, int gy_dtype, const uint8_t *packed,
                                            int layout, const GammaMap &gamma, int64_t M, int64_t N,
-                                           int64_t K, void *grad_x, int gx_dtype, hipStream_t stream);
+                                           int64_t K, void *grad_x, int gx_dtype, float *workspace,
+                                           hipStream_t stream);
+size_t backward_input_segmented_workspace(int64_t M, int64_t N, int64_t K, int gy_dtype);
 // out[0 : count) = 0 (a kernel, so it can be captured in a graph).
 hipError_t launch_zero_f32(float *out, int64_t count, hipStream_t stream);
 hipError_t launch_zero(void *out, int dtype, int64_t count, hipStream_t stream);

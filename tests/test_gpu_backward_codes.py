@@ -1,7 +1,9 @@
 """Weight gradients from INT8 codes and input gradients over stacks, against 64-bit
-products. Every product term is exact in fp32 (grad_w's factor after the two
-roundings that define it), so a sum of n terms is off by at most n u times the sum
-of their absolute values, in any order."""
+products. A term's factor is exact, or rounded twice by definition (grad_w's), and
+enters in up to three pieces that leave out at most 2^-22 = 4 u of it (fp16 pieces of
+a large problem; below fp16's normal range 2^-39 of the row's largest factor). Each
+piece's product is exact in fp32, so a sum over n factors is off by at most 3 n u times
+the sum of the terms' absolute values, in any order, besides the factors' own 6 u."""
 import pytest
 import torch
 
@@ -18,7 +20,8 @@ def bl():
     return bitlinear
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 8, 16), (5, 3, 7), (32, 256, 256), (33, 264, 272), (100, 1003, 2001),
+# (problems of both tile sizes, and of both with several workgroups a tile)
+@pytest.mark.parametrize("M,N,K", [(512, 2048, 2064), (130, 3000, 3001), (2048, 300, 520), (4096, 1030, 1000), (1, 1, 1), (1, 8, 16), (5, 3, 7), (32, 256, 256), (33, 264, 272), (100, 1003, 2001),
                                    (64, 130, 15), (250, 257, 300), (1000, 72, 80), (77, 4100, 4112), (4096, 64, 48)])
 @pytest.mark.parametrize("gy,gw", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 def test_weight(bl, M, N, K, gy, gw):
@@ -28,9 +31,10 @@ def test_weight(bl, M, N, K, gy, gw):
     got = bl.bitlinear_backward_weight_codes(grad_y, xq, scale, TYPES[gw])
     v = grad_y.cpu().double() * (scale.cpu().double() / 127)[:, None]
     want, terms = v.t() @ xq.cpu().double(), v.abs().t() @ xq.cpu().double().abs()
-    # three pieces a term of one sign; or two, which leave out less than 2^-15
-    rel = (3 * M + 4) * U if gw == "f32" else 2.0 ** -15 + (2 * M + 4) * U
-    ref.close(got, want, rel * terms, "grad_w")
+    # grad_w in bf16: two bf16 pieces, which leave out less than 2^-15, or one of fp16, 2^-12
+    rel = (3 * M + 6) * U if gw == "f32" else 2.0 ** -12 + (2 * M + 4) * U
+    least = 2.0 ** -39 * v.abs().amax(0)[:, None] * xq.cpu().double().abs().sum(0)
+    ref.close(got, want, rel * terms + least, "grad_w")
 
 
 def test_weight_pieces_carry_every_bit(bl):
@@ -46,8 +50,28 @@ def test_weight_pieces_carry_every_bit(bl):
         ref.close(got, want, 6 * U * want.abs(), "grad_w")
 
 
+def test_weight_of_wide_range(bl):
+    """Columns of any magnitude beside each other, zeros and single large tokens among
+    them, in a problem of large tiles: each is scaled by its own power of two."""
+    M, N, K = 300, 4096, 4096
+    assert bl.bitlinear_backward_weight_codes_workspace_bytes(M, N, K) > 0
+    g = torch.Generator(device="cuda").manual_seed(8)
+    grad_y = torch.randn(M, N, generator=g, device="cuda") * torch.logspace(-34, 30, N, device="cuda")
+    grad_y[:, ::7] = 0
+    grad_y[17, 1::5] *= 1000.0
+    xq, scale = bl.bitlinear_quant_acts(torch.randn(M, K, generator=g, device="cuda"))
+    got = bl.bitlinear_backward_weight_codes(grad_y, xq, scale).cpu()
+    v = grad_y.cpu().double() * (scale.cpu().double() / 127)[:, None]
+    want, terms = v.t() @ xq.cpu().double(), v.abs().t() @ xq.cpu().double().abs()
+    least = 2.0 ** -39 * v.abs().amax(0)[:, None] * xq.cpu().double().abs().sum(0)
+    # (and what fp32 holds at all: products below 2^-126 lose bits)
+    ref.close(got, want, (3 * M + 6) * U * terms + least + M * 2.0 ** -126, "grad_w")
+    assert not got[::7].any()
+
+
 STACKS = [([256, 256], 256, 256), ([8], 5, 16), ([1], 1, 1), ([3, 5, 1, 9, 2, 40, 7, 33], 20, 77), ([1003, 500, 500], 200, 3000),
-          ([72, 200], 130, 264), ([64, 64, 64], 257, 300), ([700, 704], 1000, 520), ([512, 512], 64, 4112)]
+          ([72, 200], 130, 264), ([64, 64, 64], 257, 300), ([700, 704], 1000, 520), ([512, 512], 64, 4112),
+          ([2000, 1000], 2100, 2056), ([4096], 512, 2050), ([4100, 4097], 300, 1500)]
 
 
 @pytest.mark.parametrize("segs,M,K", STACKS)
@@ -63,8 +87,10 @@ def check_input(bl, p, grad_y, gx):
     v = grad_y.cpu().double() * p.row_gamma
     want, terms = v @ p.codes.double(), v.abs() @ p.codes.double().abs()
     # rescaling: a ratio and its product where a segment ends, gamma's at the end
-    n = (3 if grad_y.dtype is F32 else 1) * sum(p.segs) + 3 * len(p.segs) + 2
-    ref.close(got, want, n * U * terms, "grad_x")
+    n = (3 if grad_y.dtype is F32 else 1) * sum(p.segs) + 3 * len(p.segs) + 6
+    least = 2.0 ** -39 * grad_y.cpu().double().abs().amax(1)[:, None] * (
+        p.row_gamma[:, None] * p.codes.double().abs()).sum(0) if grad_y.dtype is F32 else 0.0
+    ref.close(got, want, n * U * terms + least, "grad_x")
 
 
 @pytest.mark.parametrize("gammas", [[0.0, 1.0, 2.0], [2.0, 0.0, 0.5], [0.0, 0.0, 0.0], [1e30, 1e-30, 1.0], [1.0, 1.0, 1.0],
