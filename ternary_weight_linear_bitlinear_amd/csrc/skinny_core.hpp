@@ -621,6 +621,28 @@ hipError_t launch_skinny_l(const int8_t *xq, const float *scale, const uint8_t *
     if (M <= 4)
         return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 1, 4, YT>(xq, scale, packed, gamma, M, N, K,
                                                                y, acc, s, ep);
+    // A gated stack's two matrices make more rows than one round of workgroups takes in
+    // two or three row groups, and each further round stages the activations again. With
+    // more than eight tokens four or six groups are faster (two groups -> these; 16
+    // tokens, K = 4096, 2-bit / base-3 / 1-bit): 2 x 8192 rows, four, 9.0 -> 8.6 / 14.1 ->
+    // 10.6 / 7.6 -> 7.7 us; 2 x 11008 rows, six, 12.5 -> 10.3 / 19.9 -> 13.2 / 11.4 -> 9.6 us; 2
+    // x 14336 rows, four, 14.4 -> 11.7 / 25.5 -> 18.9 / 13.5 -> 11.2 us; 40 tokens, 2 x 11008 rows, six,
+    // 24.5 -> 18.7 (2-bit) / 23.3 -> 18.4 us (1-bit). Base-3 rows of several rounds spill with more than
+    // three (2 x 11008 x 8192: two 28.8, three 24.8, four 36.2 us). At eight tokens they were
+    // between 2% faster and 9% slower.
+    if constexpr (E::kGated) {
+        const bool mr = row_bytes_of(LAYOUT, K) / SkinnyCfg<LAYOUT>::kUnitBytes > (int64_t)kSkKS * kSkNSS * 4;
+        if (M > 8 && N > 16 * 256 * 3) {
+            if (LAYOUT == kLayoutBase3 && mr)
+                return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 3, 16, YT>(xq, scale, packed, gamma, M, N, K, y,
+                                                                       acc, s, ep);
+            if (N > 16 * 256 * 4 && N <= 16 * 256 * 6)
+                return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 6, 16, YT>(xq, scale, packed, gamma, M, N, K, y,
+                                                                       acc, s, ep);
+            return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 4, 16, YT>(xq, scale, packed, gamma, M, N, K, y, acc,
+                                                                   s, ep);
+        }
+    }
     // up to 16 x 256 x 3 rows: three row groups, so that one round of
     // workgroups (at most one per compute unit) covers the matrix
     const bool one_chunk = M <= 16;  // larger batches run as several 16-token chunks
@@ -1033,6 +1055,14 @@ hipError_t launch_linear_t(const XT *x, const uint8_t *packed, const GammaMap &g
                 x, packed, gamma, M, N, K, (N + 63) / 64, y, acc, s, ep);
         return launch_linear_m<LAYOUT, kFusedMaxM, 4, 4, false, XT, YT, 2>(
             x, packed, gamma, M, N, K, (N + 31) / 32, y, acc, s, ep);
+    }
+    // (gated, two to four tokens over 8192 rows and more: two row groups of eight waves;
+    // 4 tokens, 2 x 4096 x 4096, 2-bit 8.0 -> 6.9 us, base-3 9.9 -> 8.5 us, 1-bit 8.0 -> 6.9 us;
+    // 2 x 7000 x 9000, 2-bit 31.6 -> 22.2 us; 2 x 6144 x 4096 within 2%, base-3 4% slower)
+    if constexpr (E::kGated) {
+        if (M > 1 && N >= kSkRG2MinN)
+            return launch_linear_m<LAYOUT, kFusedMaxM, kFdKS, kFdNSS, false, XT, YT, 2>(
+                x, packed, gamma, M, N, K, (N + 31) / 32, y, acc, s, ep);
     }
     if (M > 1 && K % 16 == 0 &&
         K <= (int64_t)kFsKS * kFsNSS * 4 * SkinnyCfg<LAYOUT>::kUnitCodes) {
