@@ -938,6 +938,8 @@ def _kept(where, kept, M, K, dev, t):
         kept = Checkpoint(torch.empty(M, K, dtype=torch.int8, device=t.device),
                           torch.empty(shape, dtype=_f32, device=t.device))
         return kept, kept.codes.data_ptr(), kept.scale.data_ptr()
+    if not isinstance(kept, tuple) or len(kept) != 2:
+        _refuse(where, f"kept is {type(kept).__name__}, not a Checkpoint")
     codes, scale = kept
     return kept, _addr(where, "kept.codes", codes, (M, K), torch.int8, dev), \
         _addr(where, "kept.scale", scale, shape, _f32, dev)
@@ -1102,11 +1104,13 @@ def bitlinear_checkpoint(x: torch.Tensor, kept: Checkpoint | None = None, stream
 def bitlinear_checkpoint_restore(kept: Checkpoint, out_dtype=None, y: torch.Tensor | None = None,
                                  stream=None) -> torch.Tensor:
     """The kept values as a tensor [M, K] (out_dtype: y's type by default, then fp32)."""
+    where = "bitlinear_checkpoint_restore"
+    if not isinstance(kept, tuple) or len(kept) != 2:
+        _refuse(where, f"kept is {type(kept).__name__}, not a Checkpoint")
     codes = kept[0]
     if stream is not None:
-        with _on("bitlinear_checkpoint_restore", stream, codes):
+        with _on(where, stream, codes):
             return bitlinear_checkpoint_restore(kept, out_dtype, y)
-    where = "bitlinear_checkpoint_restore"
     if codes.dim() != 2:
         _refuse(where, f"kept.codes has shape {tuple(codes.shape)}")
     (M, K), dev = codes.shape, codes.get_device()

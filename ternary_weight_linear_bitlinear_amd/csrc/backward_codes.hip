@@ -329,8 +329,9 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         }
     };
     // Other rows load unaligned pieces, which run on past a row's or a segment's end into
-    // what follows; where nothing does, at the end of the matrix, element by element. A
-    // row of 16 elements more is enough: 16 rows hold them at least.
+    // what follows; where too little does, at the end of the matrix, element by element.
+    // (Behind a piece of a [p][i] tile up to 15 elements: 16 rows hold them at least.
+    // Behind one of an [i][p] tile up to BP: the rows after the tile's have to.)
     auto load_a_any = [&](int c, int64_t p0, int64_t p1) __attribute__((always_inline)) {
         const int row = ar + c * A_STEP;
         if constexpr (A_T) {
@@ -342,7 +343,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
                 const int64_t i = i0 + 8 * ac;
                 load8_some(A + p * a.lda + (i < a.I ? i : 0), i < a.I ? a.I - i : 0, a_reg[c]);
             }
-        } else if (i0 + T::BI < a.I || p0 + T::BP <= a.lda) {
+        } else if (p0 + T::BP <= a.lda || (a.I - i0 - T::BI) * a.lda >= T::BP) {
             const GT *at = a_base[A_T ? 0 : c] + p0;
             load_any(reinterpret_cast<const GT *>(reinterpret_cast<const char *>(at) + a_off[c]), a_reg[c]);
         } else {
@@ -760,14 +761,16 @@ CodesPlan codes_plan(int64_t I, int64_t J, int64_t P, int kind) {
     const double slices = (double)((P + 63) / 64), out = (double)I * (double)J;
     const double peaks = kind == kStored ? 0.0 : 6.0 + (double)I * (double)P * (kind == kInput32 ? 4e-6 : 2e-6) / 3;
     auto tiles = [&](int64_t side) { return (double)((I + side - 1) / side) * (double)((J + side - 1) / side); };
-    CodesPlan best{true, 1};
+    CodesPlan best{false, 1};
     double least = 1e30;
     for (int n = 1; n <= 16 && n <= slices; ++n) {
         const double share = std::ceil(slices / n), sums = n > 1 ? 5.0 + out * 8e-6 / 5 * n : 0.0;
         const double large = std::ceil(tiles(256) * n / 256) * (share + 2.5) * c.large + peaks + sums;
         const double alone = std::ceil(tiles(64) * n / (256 * c.side)) * (share + 1.5) * c.small;
         const double small = std::fmax(alone, tiles(64) * slices * c.full / 256) + sums;
-        if (large < least) least = large, best = {true, n};
+        // (the search for columns' largest values takes eight of them at a time)
+        const bool fits = (kind != kWeight32 && kind != kWeight16) || I >= 8;
+        if (fits && large < least) least = large, best = {true, n};
         if (small < least) least = small, best = {false, n};
     }
     return best;

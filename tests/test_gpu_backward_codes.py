@@ -22,7 +22,7 @@ def bl():
 
 # (problems of both tile sizes, and of both with several workgroups a tile)
 @pytest.mark.parametrize("M,N,K", [(512, 2048, 2064), (130, 3000, 3001), (2048, 300, 520), (4096, 1030, 1000), (1, 1, 1), (1, 8, 16), (5, 3, 7), (32, 256, 256), (33, 264, 272), (100, 1003, 2001),
-                                   (64, 130, 15), (250, 257, 300), (1000, 72, 80), (77, 4100, 4112), (4096, 64, 48)])
+                                   (64, 130, 15), (300, 5, 70000), (250, 257, 300), (1000, 72, 80), (77, 4100, 4112), (4096, 64, 48)])
 @pytest.mark.parametrize("gy,gw", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 def test_weight(bl, M, N, K, gy, gw):
     g = torch.Generator(device="cuda").manual_seed(M + N)
@@ -69,7 +69,7 @@ def test_weight_of_wide_range(bl):
     assert not got[::7].any()
 
 
-STACKS = [([256, 256], 256, 256), ([8], 5, 16), ([1], 1, 1), ([3, 5, 1, 9, 2, 40, 7, 33], 20, 77), ([1003, 500, 500], 200, 3000),
+STACKS = [([5], 65, 200), ([3, 6], 129, 64), ([256, 256], 256, 256), ([8], 5, 16), ([1], 1, 1), ([3, 5, 1, 9, 2, 40, 7, 33], 20, 77), ([1003, 500, 500], 200, 3000),
           ([72, 200], 130, 264), ([64, 64, 64], 257, 300), ([700, 704], 1000, 520), ([512, 512], 64, 4112),
           ([2000, 1000], 2100, 2056), ([4096], 512, 2050), ([4100, 4097], 300, 1500)]
 
@@ -124,3 +124,24 @@ def test_empty(bl):
                                                torch.empty(0, 64, dtype=torch.int8, device="cuda"),
                                                torch.empty(0, device="cuda"), dtype)
         assert w.shape == (24, 64) and w.dtype is dtype and not w.any()
+
+
+def test_gradients_are_the_derivatives(bl):
+    """Against differences of the 64-bit loss sum(grad_y * y), y = (xq scale / 127) (gamma
+    codes)^T: it is linear in the weights and in the input, so a difference of any step is the
+    derivative. Its error is what the gradients' own bounds make of the direction."""
+    M, K, segs = 60, 150, [70, 41]
+    p = Packed(bl, M, segs, K, seed=12)
+    gy = p.rand(M, sum(segs), scale=1e-2)
+    x = p.xq.cpu().double() * (p.scale.cpu().double() / 127)[:, None]
+    W, g64 = p.codes.double() * p.row_gamma[:, None], gy.cpu().double()
+    loss = lambda x, W: (g64 * (x @ W.t())).sum()  # noqa: E731
+    gw = bl.bitlinear_backward_weight_codes(gy, p.xq, p.scale).cpu().double()
+    gx = bl.bitlinear_backward_input_segmented(gy, p.packed, p.gammas, segs, K).cpu().double()
+    r = torch.Generator().manual_seed(3)
+    for _ in range(4):
+        D, E = torch.randn(W.shape, generator=r, dtype=torch.float64), torch.randn(x.shape, generator=r, dtype=torch.float64)
+        dw, dx = (loss(x, W + D) - loss(x, W - D)) / 2, (loss(x + E, W) - loss(x - E, W)) / 2
+        tw = (D.abs() * ((3 * M + 7) * U * (g64.abs().t() @ x.abs()))).sum()
+        tx = (E.abs() * ((3 * sum(segs) + 12) * U * (g64.abs() @ W.abs()))).sum()
+        assert (gw * D).sum().sub(dw).abs() <= tw + 1e-12 and (gx * E).sum().sub(dx).abs() <= tx + 1e-12
