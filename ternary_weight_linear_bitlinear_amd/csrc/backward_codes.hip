@@ -188,14 +188,17 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     const int nseg = A_T ? 1 : a.gm.nseg;
     if constexpr (!A_T) {
         if (tid < nseg) {
+            // (magnitudes compared as integers, which is an order of every gamma, NaN
+            // too: each segment has a rank of its own)
             const float mine = a.gm.g[tid];
+            auto size = [](float g) { return __float_as_uint(g) & 0x7FFFFFFFu; };
             int rank = 0;
             float before = 0.f;  // of the largest |gamma| that goes before
             for (int s = 0; s < nseg; ++s) {
                 const float g = a.gm.g[s];
-                if (fabsf(g) < fabsf(mine) || (fabsf(g) == fabsf(mine) && s < tid)) {
+                if (size(g) < size(mine) || (size(g) == size(mine) && s < tid)) {
                     ++rank;
-                    if (fabsf(g) >= fabsf(before)) before = g;
+                    if (size(g) >= size(before)) before = g;
                 }
             }
             seg_begin[rank] = tid == 0 ? 0 : a.gm.bound[tid - 1];
@@ -682,10 +685,9 @@ __global__ __launch_bounds__(256) void codes_peak_cols_kernel(const GT *grad_y, 
     for (int i = 1; i < 8; ++i) t = fmaxf(t, red[i][threadIdx.x]);
     peak[blockIdx.y * N + n0 + threadIdx.x] = t;
 }
-// The largest |grad_y| of each row (fp32).
-__global__ __launch_bounds__(256) void codes_peak_rows_kernel(const float *grad_y, int64_t N, float *peak) {
-    __shared__ float red[4];
-    const float *row = grad_y + (int64_t)blockIdx.x * N;
+// The largest |grad_y| of each row (fp32): a workgroup for every row, or every
+// gridDim.x-th.
+__device__ __forceinline__ void peak_row(const float *row, int64_t N, float *peak, float (&red)[4]) {
     float top = 0.f;
     if (N % 4 == 0) {
         for (int64_t n = (int64_t)threadIdx.x * 4; n < N; n += 1024) {
@@ -698,7 +700,15 @@ __global__ __launch_bounds__(256) void codes_peak_rows_kernel(const float *grad_
     top = wave_max0_dpp(top);
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top;
     __syncthreads();
-    if (threadIdx.x == 0) peak[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    if (threadIdx.x == 0) *peak = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+__global__ __launch_bounds__(256) void codes_peak_rows_kernel(const float *grad_y, int64_t M, int64_t N,
+                                                              float *peak) {
+    __shared__ float red[4];
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        peak_row(grad_y + m * N, N, peak + m, red);
+        __syncthreads();
+    }
 }
 
 // out = the sum of `splits` partial results, in order.
@@ -815,8 +825,10 @@ hipError_t launch_peaks(const CodesArgs &a, float *peak, hipStream_t s) {
         else
             hipLaunchKernelGGL((codes_peak_cols_kernel<GT, false>), grid, dim3(256), 0, s, g, a.scale, a.P, a.I, peak);
     } else {
-        hipLaunchKernelGGL(codes_peak_rows_kernel, dim3((unsigned)a.I), dim3(256), 0, s,
-                           static_cast<const float *>(a.A), a.P, peak);
+        // (2^24 workgroups of 256 would be one thread more than a launch can count)
+        const int64_t rows = a.I < 1 << 20 ? a.I : 1 << 20;
+        hipLaunchKernelGGL(codes_peak_rows_kernel, dim3((unsigned)rows), dim3(256), 0, s,
+                           static_cast<const float *>(a.A), a.I, a.P, peak);
     }
     return hipGetLastError();
 }

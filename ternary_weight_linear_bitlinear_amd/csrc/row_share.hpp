@@ -105,17 +105,18 @@ __device__ __forceinline__ void store_share(T *row, int j, const Share<J, VEC> &
 }
 
 // Eight kept codes as loaded, with their group's scale: q * (scale / 127). A code
-// plus 128 is an unsigned byte, which the hardware converts without a shift, and
-// (q + 128) f - 128 f in one fused operation is q f rounded once.
+// plus 128 is an unsigned byte, which the hardware converts without a shift. (Less
+// 128 before the product: 128 scale / 127 may be past fp32's range where the value
+// is not.)
 struct Kept8 {
     uint2 a;
     float s;
     __device__ __forceinline__ void widen(float v[8]) const {
-        const float f = s / 127.0f, off = -128.0f * f;
+        const float f = s / 127.0f;
         const uint32_t w[2] = {a.x ^ 0x80808080u, a.y ^ 0x80808080u};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = __builtin_fmaf((float)((w[e / 4] >> (8 * (e % 4))) & 0xFFu), f, off);
+            v[e] = ((float)((w[e / 4] >> (8 * (e % 4))) & 0xFFu) - 128.0f) * f;
     }
 };
 // One chunk (J = 1) of a kept row. `scale` holds the row's groups; `group` is the

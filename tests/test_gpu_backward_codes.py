@@ -106,6 +106,18 @@ def test_input_gammas(bl, gammas):
     ref.close(got, want, (212 + 11) * U * terms + 2.0 ** -120, "grad_x")
 
 
+@pytest.mark.parametrize("gy", ["f32", "bf16"])
+def test_input_of_a_gamma_that_is_no_number(bl, gy):
+    """Every segment keeps its place: the call ends, with NaN everywhere, and the next one is right."""
+    nan = float("nan")
+    for gammas in ([nan, 1.0, 2.0], [1.0, nan, nan], [nan] * 3, [float("inf"), nan, 0.0]):
+        p = Packed(bl, 0, [100, 72, 41], 96, seed=3, gammas=gammas)
+        grad_y = p.rand(50, 213, dtype=TYPES[gy])
+        got = bl.bitlinear_backward_input_segmented(grad_y, p.packed, p.gammas, p.segs, 96)
+        assert bool(got.isnan().all())
+    check_input(bl, Packed(bl, 0, [100, 72, 41], 96, seed=3), grad_y, F32)
+
+
 def test_input_of_one_segment_is_the_plain_call(bl):
     p = Packed(bl, 0, [264], 528, seed=9)
     grad_y = p.rand(70, 264, dtype=BF16, scale=1e-3)

@@ -62,3 +62,25 @@ def test_buffers_are_filled_and_nothing_else(bl):
 def test_empty(bl):
     kept = bl.bitlinear_checkpoint(torch.empty(0, 70, device="cuda"))
     assert kept.scale.shape == (0, 2) and bl.bitlinear_checkpoint_restore(kept).shape == (0, 70)
+
+
+def test_the_largest_values(bl):
+    """Up to the largest finite values of both types: 128 scale / 127 is past fp32's range.
+    (127 fl(scale / 127) itself is, by its definition, where the quotient was rounded up from
+    the last value, (2 - 2^-23) 2^127: codes of 127 in such a group alone may be infinite.)"""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = (torch.rand(5, 200, generator=g, device="cuda") * 2 - 1) * 3.4e38
+    x[0, 3], x[1, 70] = torch.finfo(F32).max, -torch.finfo(F32).max
+    codes, scale = gr.quantised(x)
+    y = bl.bitlinear_checkpoint_restore(bl.Checkpoint(codes.cuda(), scale.cuda()))
+    same = torch.equal(y.cpu(), gr.restored(codes, scale))
+    last = (scale == torch.finfo(F32).max).repeat_interleave(64, 1)[:, :200] & (codes.abs() == 127)
+    inside = bool((y.cpu().isfinite() | last).all())
+    assert same and inside
+    z = torch.full((2, 128), torch.finfo(BF16).max, device="cuda")
+    z[1] = -z[1]
+    kept = bl.Checkpoint(*(t.cuda() for t in gr.quantised(z)))
+    y = bl.bitlinear_gated_backward(torch.full((1, 128), 2.0 ** -20, device="cuda"), kept, "relu").grad_z
+    want = gr.restored(*gr.quantised(z))
+    same = [torch.equal(y.cpu()[0, 128:], want[0] * 2.0 ** -20), torch.equal(y.cpu()[0, :128], want[1] * 2.0 ** -20)]
+    assert all(same)
