@@ -20,8 +20,11 @@
 //   piece, 2^-11, for grad_w in bf16). fp16's range is short, so each row of C's values
 //   of A are scaled by a power of two that brings the largest to 2^14 .. 2^15, and the
 //   result back: a first kernel finds the largest.
-// Large tiles, bound by the matrix cores, take fp16; small ones, bound by latency, bf16
-// in one launch less.
+// Large tiles, bound by the matrix cores, take fp16 (weight gradient 4096^3 to fp32: 304 us
+// with three bf16 pieces; two fp16 ones, with loads from buffers, 239 us and 9 us for the
+// search); small ones, bound by
+// latency, bf16 in one launch less (fp16 in them: 100 x 1003 x 2001 9.6 -> 11.7 us, 200 tokens
+// over 2003 rows of 3000 29.6 -> 32.6 us).
 //
 // Each segment's sum has a factor of its own. Instead of a second set of sums the
 // running sums are rescaled where a segment ends, by the ratio of its gamma to the
@@ -32,6 +35,15 @@
 // The operands go through LDS in their natural layout, two stages of it; fragments
 // whose contraction index runs along LDS rows are read with the transposing load,
 // as in backward.hip.
+//
+// What bounds it: large tiles keep the matrix cores busy for 57-60% of a compute unit's
+// cycles at the clock that their power leaves (weight gradient 4096^3: 2 x 137 GFLOP in 239 us,
+// 1.15 PFLOP/s; input gradient of 2048 tokens over 2 x 11008 rows of 4096: 369 GFLOP in 297
+// us, 1.24 PFLOP/s; a library product of 8192^3 in bf16 reaches 1.2). Small tiles wait: of a
+// stage's 0.8 us (fp32, three pieces, aligned) 0.2 are loads and their addresses, 0.2 the
+// conversion, and the matrix cores' third hides behind the rest. Tried there and not
+// kept: loads two stages ahead (the same times), a stage's fragments read at once (29.5 -> 31.8 us),
+// half as long slices and twice the workgroups (27 -> 31 us for 300 tokens over 2 x 2000 rows).
 #include "backward_util.hpp"
 #include "bl_internal.hpp"
 #include "device_util.hpp"
@@ -754,32 +766,44 @@ struct KindOf {
 
 // How a product runs: 256 x 256 tiles or 64 x 64 ones, and the workgroups that share
 // a tile's slices where there are few tiles: whichever takes the least time by a model
-// of what was measured (64 contraction indexes in us; fixed costs in them too).
-//   large tiles: a round of one for each compute unit, `large` us;
-//   small tiles: `small` us alone, `full` for each where they fill the card, up to
-//   three (two) of them side by side;
-//   partial sums: written and read at 5 TB/s, and a launch more; the search for the
-//   largest values of fp16 pieces: a launch, and A read at 3 TB/s.
+// whose constants were fitted to 5982 problems of 8 to 4096 tokens and up to 4096 x 21000
+// weights, each timed with both tiles and every number of workgroups below. What it picks
+// takes 0.9% (weight gradients), 1.8% (input gradients of fp32) and 2.8% (of bf16) more on
+// average than the fastest choice for each of them.
+//   Small tiles: us for 64 contraction indexes with one workgroup on a compute unit, with
+//   more, and for each where they fill the card; large ones: us for a round of one for each
+//   compute unit. What a workgroup does besides counts as so many slices more. Rows that
+//   are loaded unaligned take a factor.
+//   Partial sums: a launch, and 5 TB/s; the search for the largest values of fp16 pieces: a
+//   launch, and A read at 3 TB/s.
 struct CodesPlan {
     bool large;
     int splits;
 };
 CodesPlan codes_plan(int64_t I, int64_t J, int64_t P, int kind) {
-    static const struct { double large, small, full; int side; } kCost[4] = {
-        {1.6, 0.47, 0.28, 3}, {2.9, 1.5, 0.8, 3}, {1.95, 0.97, 0.55, 2}, {2.75, 0.8, 0.55, 2}};
+    static const struct { double one, more, full, start, ragged, large, large_start, large_ragged; } kCost[4] = {
+        {0.43, 0.59, 0.33, 4.55, 1.63, 1.73, 3.05, 1.69},
+        {1.59, 2.22, 1.09, 0.81, 1.26, 3.60, 2.83, 1.46},
+        {0.81, 1.05, 0.70, 1.60, 1.69, 2.22, 1.89, 2.52},
+        {0.73, 0.93, 0.60, 3.36, 1.52, 1.94, 2.52, 2.05}};
     const auto &c = kCost[kind];
+    const bool weight = kind == kWeight32 || kind == kWeight16;
+    const bool ragged = weight ? I % 8 != 0 || J % 16 != 0 : P % 8 != 0;
     const double slices = (double)((P + 63) / 64), out = (double)I * (double)J;
-    const double peaks = kind == kStored ? 0.0 : 6.0 + (double)I * (double)P * (kind == kInput32 ? 4e-6 : 2e-6) / 3;
+    const double peaks = kind == kStored ? 0.0 : 4.0 + (double)I * (double)P * (kind == kInput32 ? 4e-6 : 2e-6) / 3;
     auto tiles = [&](int64_t side) { return (double)((I + side - 1) / side) * (double)((J + side - 1) / side); };
+    // (the search for columns' largest values takes eight of them at a time)
+    const bool fits = out >= 32768 && (!weight || I >= 8);
     CodesPlan best{false, 1};
-    double least = 1e30;
-    for (int n = 1; n <= 16 && n <= slices; ++n) {
-        const double share = std::ceil(slices / n), sums = n > 1 ? 5.0 + out * 8e-6 / 5 * n : 0.0;
-        const double large = std::ceil(tiles(256) * n / 256) * (share + 2.5) * c.large + peaks + sums;
-        const double alone = std::ceil(tiles(64) * n / (256 * c.side)) * (share + 1.5) * c.small;
-        const double small = std::fmax(alone, tiles(64) * slices * c.full / 256) + sums;
-        // (the search for columns' largest values takes eight of them at a time)
-        const bool fits = (kind != kWeight32 && kind != kWeight16) || I >= 8;
+    double least = 1e300;
+    for (int n : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (n > 1 && (n > slices || n * out > 125e6)) break;  // (half a gigabyte of partial sums)
+        const double share = std::ceil(slices / n), sums = n > 1 ? 2.5 + out * 1.6e-6 * n : 0.0;
+        const double large = std::ceil(tiles(256) * n / 256) * (share + c.large_start) * c.large *
+                                 (ragged ? c.large_ragged : 1.0) + peaks + sums;
+        const double each = tiles(64) * n / 256;
+        const double small = (share + c.start) * std::fmax(each <= 1 ? c.one : c.more, c.full * each) *
+                                 (ragged ? c.ragged : 1.0) + sums;
         if (fits && large < least) least = large, best = {true, n};
         if (small < least) least = small, best = {false, n};
     }

@@ -289,7 +289,10 @@ struct RowEpilogue {
 // col + BN / 2 - 1 and then the same up rows, so that a thread finishes eight
 // output columns of a token from a piece of either half. Kept in 8 bits, eight
 // threads side by side hold a checkpoint group of 64 columns (tiles begin at
-// multiples of 64) and take its maximum across lanes.
+// multiples of 64) and take its maximum across lanes. 2048 x 2 x 11008 x 4096, 2-bit, silu:
+// 180 us, 2.05 POP/s (a library INT8 product of 8192^3: 2.1), with bias and the checkpoint
+// 194 us; as a stack's product with z stored and an elementwise pass they would move 180 MB
+// more.
 template <int BN, int T, typename YT>
 struct GatedRows {
     static constexpr int kPieces = BN / 16, kStep = T / kPieces;
