@@ -865,6 +865,7 @@ hipError_t launch_codes_kind(CodesArgs a, bool vec, float *workspace, hipStream_
     // (a stage of three pieces of a [p][i] tile of 64 would leave one workgroup to a
     // compute unit: 1024 tiles 1.1 us each and none side by side)
     using Small = Tile<64, 64, KIND == kWeight32 ? 32 : 64, 2, 2>;
+    static_assert(Large::BP <= 64 && Small::BP <= 64, "the plan's slices of 64: a workgroup has at least one");
     const CodesPlan plan = codes_plan(a.I, a.J, a.P, KIND);
     a.splits = plan.splits;
     if constexpr (K::kHalf) {
