@@ -451,7 +451,7 @@ bl_status bitlinear_linear_gated(const void *x, int x_dtype, const uint8_t *pack
 }
 
 size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F) {
-    if (M < 1 || F < 1 || 2 * M > kMaxDim || 2 * F > kMaxDim) return 0;
+    if (M < 1 || F < 1 || M > kMaxDim / 2 || F > kMaxDim / 2) return 0;
     return (size_t)(bl::gated_grad_parts(M, F) * 2 * F) * sizeof(float);
 }
 
@@ -489,7 +489,7 @@ bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void 
     return launched(bl::launch_gated_backward(a, s));
 }
 
-int64_t bitlinear_checkpoint_groups(int64_t K) { return K < 1 ? 0 : bl::checkpoint_groups(K); }
+int64_t bitlinear_checkpoint_groups(int64_t K) { return K < 1 ? 0 : (K - 1) / bl::kCheckpointGroup + 1; }
 
 bl_status bitlinear_checkpoint(const void *x, int x_dtype, int64_t M, int64_t K, int8_t *codes,
                                float *scale, void *stream) {

@@ -244,3 +244,10 @@ def test_counts_are_read_at_each_call(bl):
     rows[0] += 1
     with pytest.raises(bl.BitLinearError, match="16 columns for 17"):
         bl.bitlinear_backward_input_segmented(torch.ones(5, 16), torch.zeros(16, 16, dtype=torch.uint8), torch.ones(2), rows, 64)
+
+
+def test_workspace_of_the_largest_numbers_is_none(bl):
+    """2 M may not overflow on its way to the limit."""
+    for big in (2 ** 62, 2 ** 62 + 1, 2 ** 63 - 1):
+        assert bl.bitlinear_gated_backward_workspace_bytes(big, 8) == 0
+        assert bl.bitlinear_gated_backward_workspace_bytes(8, big) == 0
