@@ -363,8 +363,8 @@ bl_status bitlinear_linear_gated(const void *x, int x_dtype, const uint8_t *pack
                                  const void *bias, int bias_dtype, int act, void *z, void *y,
                                  int y_dtype, void *stream);
 
-/* Device workspace (bytes) of bitlinear_gated_backward; 0 for an empty or refused
- * shape. */
+/* Device workspace (bytes) of bitlinear_gated_backward; 0 where none is needed (few
+ * tokens), and for an empty or refused shape. */
 size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F);
 
 /* Backward of the gated epilogue:
@@ -379,7 +379,8 @@ size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F);
  *            left (exactly one of z and the pair is given).
  *   grad_z   out [M, 2F] gz_dtype, or NULL.
  *   grad_bias out [2F] fp32, or NULL: fp32 sums of the unrounded grad_z over at most
- *            512 tokens at a time, added in fp64 in a fixed order. Needs the workspace.
+ *            512 tokens at a time, added in fp64 in a fixed order. Needs the workspace
+ *            (NULL where its size is 0).
  * relu's slope at 0 is 0. At least one output is required; outputs may not overlap
  * inputs. M at most 2^23, F at most 2^23. M = 0 writes zeros to grad_bias. */
 bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void *z, int z_dtype,

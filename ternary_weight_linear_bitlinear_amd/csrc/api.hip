@@ -452,7 +452,8 @@ bl_status bitlinear_linear_gated(const void *x, int x_dtype, const uint8_t *pack
 
 size_t bitlinear_gated_backward_workspace_bytes(int64_t M, int64_t F) {
     if (M < 1 || F < 1 || M > kMaxDim / 2 || F > kMaxDim / 2) return 0;
-    return (size_t)(bl::gated_grad_parts(M, F) * 2 * F) * sizeof(float);
+    const int64_t parts = bl::gated_grad_parts(M, F);
+    return parts > 1 ? (size_t)(parts * 2 * F) * sizeof(float) : 0;
 }
 
 bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void *z, int z_dtype,
@@ -474,9 +475,8 @@ bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void 
             (z != nullptr) == (codes != nullptr))
             return BL_ERR_INVALID_ARG;
         if (!grad_z && !grad_bias) return BL_ERR_INVALID_ARG;
-        if (grad_bias &&
-            (!workspace || workspace_bytes < bitlinear_gated_backward_workspace_bytes(M, F)))
-            return BL_ERR_INVALID_ARG;
+        const size_t need = grad_bias ? bitlinear_gated_backward_workspace_bytes(M, F) : 0;
+        if (need > 0 && (!workspace || workspace_bytes < need)) return BL_ERR_INVALID_ARG;
     } else if (!grad_bias) {
         return BL_OK;
     }

@@ -20,7 +20,7 @@ def bl():
 FWD = dict(xq=P, scale=P, packed=P, layout=0, gammas=P, F=20, M=32, K=64, bias=P, bdt=0, act=3, z=P, codes=P, cs=P, y=P,
            ydt=0, stream=None)
 LIN = dict(x=P, xdt=1, packed=P, layout=0, gammas=P, F=20, M=2, K=64, bias=P, bdt=0, act=3, z=P, y=P, ydt=0, stream=None)
-BWD = dict(gy=P, gydt=0, z=P, zdt=0, codes=None, cs=None, act=3, M=8, F=20, gz=P, gzdt=0, gb=P, ws=P, wsb=1 << 20,
+BWD = dict(gy=P, gydt=0, z=P, zdt=0, codes=None, cs=None, act=3, M=200, F=20, gz=P, gzdt=0, gb=P, ws=P, wsb=1 << 20,
            stream=None)
 KEEP = dict(x=P, xdt=0, M=8, K=70, codes=P, scale=P, stream=None)
 BACK = dict(codes=P, scale=P, M=8, K=70, y=P, ydt=0, stream=None)
@@ -100,7 +100,8 @@ def test_sizes(bl):
         assert lib.bitlinear_checkpoint_groups(K) == bl.bitlinear_checkpoint_groups(K) == max(0, -(-K // 64))
     for M, F in ((0, 5), (5, 0), (-1, 5), ((1 << 23) + 1, 5), (5, (1 << 23) + 1)):
         assert bl.bitlinear_gated_backward_workspace_bytes(M, F) == 0
-    need = bl.bitlinear_gated_backward_workspace_bytes(8, 20)
+    assert bl.bitlinear_gated_backward_workspace_bytes(128, 20) == 0  # one run of rows: no partial sums
+    need = bl.bitlinear_gated_backward_workspace_bytes(200, 20)
     assert need > 0 and call(bl, "bitlinear_gated_backward", BWD, dict(wsb=need - 1)) == bl.BL_ERR_INVALID_ARG
     for M, N, K in ((0, 5, 5), (5, 0, 5), (5, 5, 0), ((1 << 24) + 1, 5, 5)):
         assert bl.bitlinear_backward_weight_codes_workspace_bytes(M, N, K) == 0
