@@ -650,8 +650,10 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
             for (int r = 0; r < 16; ++r) {
                 const int row = wi * (T::BI / T::WI) + fi * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
                 float v = acc[fi][fj][r];
-                if constexpr (!A_T) v *= alpha;
+                // (the power of two first: with it still in, gamma could take a sum that fp32
+                // holds past its range)
                 if constexpr (HALF) v *= inverse[row];
+                if constexpr (!A_T) v *= alpha;
                 if (i0 + row < a.I && j < a.J) put(C, (i0 + row) * a.J + j, v);
             }
         }
