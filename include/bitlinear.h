@@ -428,9 +428,10 @@ size_t bitlinear_backward_input_segmented_workspace_bytes(int64_t M, int64_t N, 
  *            and enters the matrix cores in 16-bit pieces; products are exact, sums fp32.
  *            BL_F32: three bf16 pieces, exact (for magnitudes >= 2^-110, as in
  *            bitlinear_backward_input), or, in large problems, two fp16 pieces scaled by
- *            a power of two for each column of grad_y: the factor to within 2^-22 of its
- *            magnitude, or 2^-39 of its column's largest where that is more. BL_BF16: two
- *            bf16 pieces (to within 2^-15) or one fp16 piece (2^-11), rounded once.
+ *            a power of two for each column of grad_y, where they hold every factor of 256
+ *            columns to within max(4, M) * 2^-24 of its own magnitude (2^-22 for all but
+ *            the smallest), less than the sum's own bound. BL_BF16: two bf16 pieces (to
+ *            within 2^-15) or one fp16 piece (2^-11), rounded once.
  * Any N and K (multiples of 8 and 16 load faster). Dimensions above 2^24 return
  * BL_ERR_INVALID_ARG. N = 0 is a no-op; M = 0 writes zeros. */
 bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, const int8_t *xq,
@@ -442,7 +443,7 @@ bl_status bitlinear_backward_weight_codes(const void *grad_y, int gy_dtype, cons
  *   grad_x[m, k] = sum_s gammas[s] * sum_{n in segment s} grad_y[m, n] * c[n, k]
  *   grad_y   [M, N] gy_dtype, N = sum(seg_rows). bf16 values are taken as they are, fp32
  *            ones as three exact bf16 pieces or, in large problems, two fp16 ones (as
- *            above, with a power of two for each row of grad_y).
+ *            above, with a power of two for each row of grad_y, to within max(4, N) * 2^-24).
  *   packed, layout, gammas, seg_rows, nseg: as in bitlinear_forward_segmented (one
  *            segment: a plain matrix).
  *   workspace as for bitlinear_backward_weight_codes.

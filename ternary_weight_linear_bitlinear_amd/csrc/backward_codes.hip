@@ -15,14 +15,18 @@
 // same fragment of B is multiplied by one after the other. Two ways:
 //   three bf16 pieces of 8 significant bits each: exact, whatever the values. grad_w in
 //   bf16 takes two of them (v to within 2^-15, far below its own rounding of 2^-8).
-//   two fp16 pieces of 11 bits, rounded to nearest: v to within 2^-22 of its magnitude
-//   (or 2^-39 of its column's largest, where that is more), for two thirds of the matrix-core work (one
-//   piece, 2^-11, for grad_w in bf16). fp16's range is short, so each row of C's values
-//   of A are scaled by a power of two that brings the largest to 2^14 .. 2^15, and the
-//   result back: a first kernel finds the largest.
-// Large tiles, bound by the matrix cores, take fp16 (weight gradient 4096^3 to fp32: 304 us
-// with three bf16 pieces; two fp16 ones, with loads from buffers, 239 us and 9 us for the
-// search); small ones, bound by
+//   two fp16 pieces of 11 bits, rounded to nearest, for two thirds of the matrix-core work
+//   (one for grad_w in bf16). fp16's range is short, so each row of C's values of A are
+//   scaled by a power of two that brings the largest to 2^14 .. 2^15, and the result back.
+//   A scaled value x is then off by 2^-22 x or 2^-25, whichever is more (one piece: 2^-11 x
+//   or 2^-25). A first kernel finds each row's largest value and the least that is not
+//   zero, and a tile takes fp16 only where no value of its rows can be off by more than
+//   max(4, P) 2^-24 of itself, what a sum of P terms in fp32 may be off by anyway (one
+//   piece: 2^-11). Other tiles take the bf16 pieces: beside a value 2^30 times theirs, whose
+//   code is zero, the rest of a row would keep eight bits.
+// Large tiles, bound by the matrix cores, take fp16 (weight gradient 4096^3 to fp32: 239 us
+// and 9 us for the search; where the values of every tile lie too far apart 327 us in all);
+// small ones, bound by
 // latency, bf16 in one launch less (fp16 in them: 100 x 1003 x 2001 9.6 -> 11.7 us, 200 tokens
 // over 2003 rows of 3000 29.6 -> 32.6 us).
 //
@@ -67,9 +71,11 @@ struct CodesArgs {
     int64_t I, J, P;
     int tiles_i, tiles_j;
     int splits;   // workgroups that share a tile's slices
-    const float *peak;  // fp16 pieces: the largest |A(i, .)|, [peaks, I]
+    const uint2 *peak;  // fp16 pieces: the largest |A(i, .)| (a float's bits) and the least
+                        // that is not zero (its least_key), [peaks, I]
     int peaks;
     void *C;      // [I, J]; with splits their partial sums, [splits, I, J] fp32
+    float floor;  // what the least one has to be where the largest is 2^14 .. 2^15
 };
 
 // Block tile BI x BJ outputs, contraction slice BP per stage, WI x WJ waves.
@@ -139,9 +145,13 @@ __device__ __forceinline__ float peak_scale(float top) {
     e = e < 15u ? 15u : e;
     return __uint_as_float((268u - e) << 23);
 }
-__device__ __forceinline__ float peak_inverse(float scale) {
+__device__ __forceinline__ float power_inverse(float scale) {
     return __uint_as_float((254u << 23) - __float_as_uint(scale));
 }
+// The order of |v| with zeros last: its bits without the sign, doubled, less one.
+__device__ __forceinline__ uint32_t least_key(float v) { return 2u * __float_as_uint(v) - 1u; }
+constexpr uint32_t kNoLeast = 0xFFFFFFFFu;
+__device__ __forceinline__ float least_of(uint32_t key) { return __uint_as_float((key + 1u) / 2u); }
 
 // Memory of `bytes` bytes (as many as 32 bits hold) from a uniform address, as buffer
 // loads take it: offsets past it read zeros.
@@ -174,7 +184,7 @@ __device__ __forceinline__ float over127(float x) {
 // the loads of the next stage at once. Fragments are read one group of
 // instructions ahead.
 template <typename T, bool A_T, int BSRC, int NP, bool HALF, bool VEC, typename GT, typename OT>
-__global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs a) {
+__device__ __forceinline__ bool codes_gemm_tile(const CodesArgs a) {
     using S = Stage<T, A_T, BSRC, NP>;
     constexpr int kT = T::kThreads;
     static_assert(A_T == (BSRC == kBCodes8), "grad_w from INT8 codes, grad_x from packed ones");
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     const int ntiles = a.tiles_i * a.tiles_j;
     const int per_xcd = (ntiles * a.splits + kXcds - 1) / kXcds;
     int t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-    if (t >= ntiles * a.splits) return;
+    if (t >= ntiles * a.splits) return true;
     const int split = t / ntiles;
     t -= split * ntiles;
     const int64_t i0 = (int64_t)(t / a.tiles_j) * T::BI;
@@ -223,9 +233,6 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         }
         __syncthreads();
     }
-
-    // fp16 pieces: scales of the thread's columns (A_T) or rows, inverses for the end
-    __shared__ float inverse[HALF ? T::BI : 1];
 
     // ---- global -> registers ------------------------------------------------------
     constexpr int A_ROW = A_T ? T::BI / 8 : T::BP / 8;  // chunks of eight in a tile row
@@ -278,18 +285,28 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
     const int b_shift = BSRC == kBPacked3 ? (int)(c0 / 5 - b_first) : BSRC == kBPacked1 ? (int)(c0 % 32 / 4) : 0;
     const int b_code = BSRC == kBPacked3 ? (int)(c0 % 5) : 0;
 
+    // fp16 pieces: the powers of two of the thread's columns (A_T) or rows, inverses for the
+    // end; and whether every row's values are near enough to its largest for them.
+    __shared__ float inverse[HALF ? T::BI : 1];
+    __shared__ int apart;
     float a_pow[HALF ? (A_T ? 8 : A_CH) : 1];
     if constexpr (HALF) {
-        // (the largest of each column over the runs: every thread takes a column's share)
+        // (over the runs: every thread takes a row's share)
         constexpr int kShares = kT / T::BI;
         static_assert(kShares >= 1 && kT % T::BI == 0, "a thread for each row of the tile");
         float *red = reinterpret_cast<float *>(smem);  // [kShares][BI]
         const int col = tid % T::BI, share = tid / T::BI;
         const int64_t i = i0 + col < a.I ? i0 + col : a.I - 1;
         float top = 0.f;
+        uint32_t least = kNoLeast;
 #pragma unroll 8
-        for (int n = share; n < a.peaks; n += kShares) top = fmaxf(top, a.peak[n * a.I + i]);
+        for (int n = share; n < a.peaks; n += kShares) {
+            const uint2 v = a.peak[n * a.I + i];
+            top = fmaxf(top, __uint_as_float(v.x));
+            least = min(least, v.y);
+        }
         red[tid] = top;
+        if (tid == 0) apart = 0;
         __syncthreads();
         auto scale_of = [&](int row) {
             float t = red[row];
@@ -299,8 +316,11 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
         };
 #pragma unroll
         for (int e = 0; e < (A_T ? 8 : A_CH); ++e) a_pow[e] = scale_of(A_T ? 8 * ac + e : ar + e * A_STEP);
-        if (tid < T::BI) inverse[tid] = peak_inverse(scale_of(tid));
+        const float scale = scale_of(col);
+        if (tid < T::BI) inverse[tid] = power_inverse(scale);
+        if (least != kNoLeast && !(least_of(least) * scale >= a.floor)) apart = 1;
         __syncthreads();  // the memory is the stages' from here on
+        if (__builtin_amdgcn_readfirstlane(apart)) return false;
     }
 
     // Aligned rows load from buffers that end with the segment: what lies past it reads
@@ -622,7 +642,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
             for (int q = g * kTasks / kGroups; q < (g + 1) * kTasks / kGroups; ++q) task(q, to, next, then, left > 2);
         }
         if (left == 1) break;
-        if (next.seg != cur.seg) {
+        if (!A_T && next.seg != cur.seg) {  // (grad_w has one segment)
             const float f = seg_ratio[next.seg];
 #pragma unroll
             for (int i = 0; i < T::FI; ++i)
@@ -657,20 +677,33 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
                 if (i0 + row < a.I && j < a.J) put(C, (i0 + row) * a.J + j, v);
             }
         }
+    return true;
 }
 
-// The largest |v| of each column of grad_y [M, N] over a run of tokens: eight columns
+// HALF: NP fp16 pieces, or EXACT bf16 ones in tiles whose rows' values lie too far apart.
+template <typename T, bool A_T, int BSRC, int NP, bool HALF, int EXACT, bool VEC, typename GT, typename OT>
+__global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs a) {
+    if (!codes_gemm_tile<T, A_T, BSRC, NP, HALF, VEC, GT, OT>(a))
+        codes_gemm_tile<T, A_T, BSRC, EXACT, false, VEC, GT, OT>(a);
+}
+
+// The largest |v| of each column of grad_y [M, N] over a run of tokens and the least that
+// is not zero: eight columns
 // and every eighth token of the run for each thread.
 template <typename GT, bool VEC>
 __global__ __launch_bounds__(256) void codes_peak_cols_kernel(const GT *grad_y, const float *scale, int64_t M,
-                                                              int64_t N, float *peak) {
+                                                              int64_t N, uint2 *peak) {
     __shared__ float red[8][256];
+    __shared__ uint32_t low[8][256];
     const int r = threadIdx.x / 32;
     const int64_t n0 = (int64_t)blockIdx.x * 256;
     const int left = (int)(N - n0 < 256 ? N - n0 : 256);
     const Share<1, VEC> sh{left, (int)threadIdx.x % 32, 32};
     const int64_t m0 = M * blockIdx.y / gridDim.y, m1 = M * (blockIdx.y + 1) / gridDim.y;
-    float top[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float top[8];
+    uint32_t lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top[e] = 0.f, lo[e] = kNoLeast;
     for (int64_t m = m0 + r; m < m1; m += 32) {
         RowRegs<GT, 1, VEC> g[4];
         float f[4];
@@ -685,42 +718,58 @@ __global__ __launch_bounds__(256) void codes_peak_cols_kernel(const GT *grad_y, 
             float v[8];
             g[u].widen(0, sh, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], fabsf(v[e] * f[u]));
+            for (int e = 0; e < 8; ++e) {
+                v[e] *= f[u];
+                top[e] = fmaxf(top[e], fabsf(v[e]));
+                lo[e] = min(lo[e], least_key(v[e]));
+            }
         }
     }
     const int start = sh.start(0), skip = sh.skip(0);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (e >= skip) red[r][start + e] = top[e];
+        if (e >= skip) red[r][start + e] = top[e], low[r][start + e] = lo[e];
     __syncthreads();
     if ((int)threadIdx.x >= left) return;
     float t = red[0][threadIdx.x];
+    uint32_t l = low[0][threadIdx.x];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t = fmaxf(t, red[i][threadIdx.x]);
-    peak[blockIdx.y * N + n0 + threadIdx.x] = t;
-}
-// The largest |grad_y| of each row (fp32): a workgroup for every row, or every
-// gridDim.x-th.
-__device__ __forceinline__ void peak_row(const float *row, int64_t N, float *peak, float (&red)[4]) {
-    float top = 0.f;
-    if (N % 4 == 0) {
-        for (int64_t n = (int64_t)threadIdx.x * 4; n < N; n += 1024) {
-            const float4 v = *reinterpret_cast<const float4 *>(row + n);
-            top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-        }
-    } else {
-        for (int64_t n = threadIdx.x; n < N; n += 256) top = fmaxf(top, fabsf(row[n]));
+    for (int i = 1; i < 8; ++i) {
+        t = fmaxf(t, red[i][threadIdx.x]);
+        l = min(l, low[i][threadIdx.x]);
     }
-    top = wave_max0_dpp(top);
-    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) *peak = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    peak[blockIdx.y * N + n0 + threadIdx.x] = make_uint2(__float_as_uint(t), l);
 }
+// The same of each row of grad_y (fp32): a workgroup for every row, or every gridDim.x-th.
 __global__ __launch_bounds__(256) void codes_peak_rows_kernel(const float *grad_y, int64_t M, int64_t N,
-                                                              float *peak) {
+                                                              uint2 *peak) {
     __shared__ float red[4];
+    __shared__ uint32_t low[4];
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        peak_row(grad_y + m * N, N, peak + m, red);
+        const float *row = grad_y + m * N;
+        float top = 0.f;
+        uint32_t lo = kNoLeast;
+        auto take = [&](float v) {
+            top = fmaxf(top, fabsf(v));
+            lo = min(lo, least_key(v));
+        };
+        if (N % 4 == 0) {
+            for (int64_t n = (int64_t)threadIdx.x * 4; n < N; n += 1024) {
+                const float4 v = *reinterpret_cast<const float4 *>(row + n);
+                take(v.x), take(v.y), take(v.z), take(v.w);
+            }
+        } else {
+            for (int64_t n = threadIdx.x; n < N; n += 256) take(row[n]);
+        }
+        top = wave_max0_dpp(top);
+#pragma unroll
+        for (int o = 32; o > 0; o /= 2) lo = min(lo, (uint32_t)__shfl_xor((int)lo, o, 64));
+        if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top, low[threadIdx.x / 64] = lo;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            peak[m] = make_uint2(__float_as_uint(top), min(min(low[0], low[1]), min(low[2], low[3])));
+        }
         __syncthreads();
     }
 }
@@ -761,9 +810,9 @@ __global__ __launch_bounds__(256) void codes_sum_kernel(const float *__restrict_
 enum CodesKind { kStored, kWeight32, kWeight16, kInput32 };  // kWeight16: grad_w in bf16
 template <int KIND>
 struct KindOf {
-    static constexpr bool kHalf = KIND != kStored;                       // in large tiles
+    static constexpr bool kHalf = KIND != kStored;  // fp16 in large tiles, kLarge pieces
     static constexpr int kLarge = KIND == kStored || KIND == kWeight16 ? 1 : 2;
-    static constexpr int kSmall = KIND == kStored ? 1 : KIND == kWeight16 ? 2 : 3;
+    static constexpr int kExact = KIND == kStored ? 1 : KIND == kWeight16 ? 2 : 3;  // bf16 pieces
 };
 
 // How a product runs: 256 x 256 tiles or 64 x 64 ones, and the workgroups that share
@@ -813,19 +862,19 @@ CodesPlan codes_plan(int64_t I, int64_t J, int64_t P, int kind) {
 }
 constexpr int64_t kPeakRuns = 64;  // of at least 32 tokens, which a workgroup loads at once
 int64_t peak_runs(int64_t M) { return M < 32 * kPeakRuns ? (M + 31) / 32 : kPeakRuns; }
-// Floats of partial sums, and of the largest values behind them.
+// Floats of partial sums; behind them the largest values and the least, in pairs.
 int64_t codes_partials(const CodesPlan &p, int64_t I, int64_t J) {
     return p.splits > 1 ? ((int64_t)p.splits * I * J + 3) / 4 * 4 : 0;
 }
 size_t codes_workspace(int64_t I, int64_t J, int64_t P, int kind) {
     const CodesPlan p = codes_plan(I, J, P, kind);
-    const int64_t peaks = !p.large || kind == kStored ? 0 : kind == kInput32 ? I : peak_runs(P) * I;
+    const int64_t peaks = !p.large || kind == kStored ? 0 : 2 * (kind == kInput32 ? I : peak_runs(P) * I);
     return (size_t)(codes_partials(p, I, J) + peaks) * sizeof(float);
 }
 
-template <typename T, bool A_T, int BSRC, int NP, bool HALF, typename GT, typename OT>
+template <typename T, bool A_T, int BSRC, int NP, bool HALF, int EXACT, typename GT, typename OT>
 hipError_t launch_codes(CodesArgs a, bool vec, hipStream_t s) {
-    using S = Stage<T, A_T, BSRC, NP>;
+    using S = Stage<T, A_T, BSRC, (EXACT > NP ? EXACT : NP)>;
     a.tiles_i = (int)((a.I + T::BI - 1) / T::BI);
     a.tiles_j = (int)((a.J + T::BJ - 1) / T::BJ);
     const int64_t blocks = ((int64_t)a.tiles_i * a.tiles_j * a.splits + kXcds - 1) / kXcds * kXcds;
@@ -836,13 +885,13 @@ hipError_t launch_codes(CodesArgs a, bool vec, hipStream_t s) {
         return hipGetLastError();
     };
     static LdsFlag lds_raised[2];
-    if (vec) return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, true, GT, OT>, &lds_raised[1]);
-    return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, false, GT, OT>, &lds_raised[0]);
+    if (vec) return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, EXACT, true, GT, OT>, &lds_raised[1]);
+    return go(codes_gemm_kernel<T, A_T, BSRC, NP, HALF, EXACT, false, GT, OT>, &lds_raised[0]);
 }
 
-// The largest |A(i, .)| in a.peak.
+// The largest |A(i, .)| and the least that is not zero, in a.peak.
 template <bool A_T, typename GT>
-hipError_t launch_peaks(const CodesArgs &a, float *peak, hipStream_t s) {
+hipError_t launch_peaks(const CodesArgs &a, uint2 *peak, hipStream_t s) {
     if constexpr (A_T) {
         const GT *g = static_cast<const GT *>(a.A);
         const dim3 grid((unsigned)((a.I + 255) / 256), (unsigned)a.peaks);
@@ -872,9 +921,13 @@ hipError_t launch_codes_kind(CodesArgs a, bool vec, float *workspace, hipStream_
     a.splits = plan.splits;
     if constexpr (K::kHalf) {
         if (plan.large) {
-            float *peak = workspace + codes_partials(plan, a.I, a.J);
+            uint2 *peak = reinterpret_cast<uint2 *>(workspace + codes_partials(plan, a.I, a.J));
             a.peaks = A_T ? (int)peak_runs(a.P) : 1;
             a.peak = peak;
+            // A value x (of 2^15 at most) is off by 2^-22 x or 2^-25, whichever is more, in two
+            // pieces: by max(4, P) 2^-24 of itself at most from this floor on, no more than a sum
+            // of P such terms in fp32. In one piece by 2^-11 x or 2^-25: from 2^-14 on 2^-11.
+            a.floor = KIND == kWeight16 ? 0x1p-14f : 0.5f / (float)(a.P < 4 ? 4 : a.P);
             const hipError_t e = launch_peaks<A_T, GT>(a, peak, s);
             if (e != hipSuccess) return e;
         }
@@ -882,8 +935,8 @@ hipError_t launch_codes_kind(CodesArgs a, bool vec, float *workspace, hipStream_
     OT *out = static_cast<OT *>(a.C);
     auto go = [&](auto *type) {
         using T = Pointee<decltype(type)>;
-        return plan.large ? launch_codes<Large, A_T, BSRC, K::kLarge, K::kHalf, GT, T>(a, vec, s)
-                          : launch_codes<Small, A_T, BSRC, K::kSmall, false, GT, T>(a, vec, s);
+        return plan.large ? launch_codes<Large, A_T, BSRC, K::kLarge, K::kHalf, K::kExact, GT, T>(a, vec, s)
+                          : launch_codes<Small, A_T, BSRC, K::kExact, false, K::kExact, GT, T>(a, vec, s);
     };
     if (plan.splits == 1) return go(out);
     a.C = workspace;
@@ -908,7 +961,7 @@ hipError_t launch_backward_weight_codes(const void *grad_y, int gy_dtype, const 
                                         const float *scale, int64_t M, int64_t N, int64_t K,
                                         void *grad_w, int gw_dtype, float *workspace,
                                         hipStream_t stream) {
-    const CodesArgs a{grad_y, N, xq, K, scale, {}, N, K, M, 0, 0, 1, nullptr, 0, grad_w};
+    const CodesArgs a{grad_y, N, xq, K, scale, {}, N, K, M, 0, 0, 1, nullptr, 0, grad_w, 0.f};
     const bool vec = N % 8 == 0 && K % 16 == 0;
     return typed(gy_dtype, [&](auto g) {
         using GT = Pointee<decltype(g)>;
@@ -923,7 +976,7 @@ hipError_t launch_backward_input_segmented(const void *grad_y, int gy_dtype, con
                                            int64_t K, void *grad_x, int gx_dtype, float *workspace,
                                            hipStream_t stream) {
     const CodesArgs a{grad_y, N, packed, row_bytes_of(layout, K), nullptr, gamma, M, K, N,
-                      0, 0, 1, nullptr, 0, grad_x};
+                      0, 0, 1, nullptr, 0, grad_x, 0.f};
     bool vec = N % 8 == 0;
     for (int s = 0; s + 1 < gamma.nseg; ++s) vec = vec && gamma.bound[s] % 8 == 0;
     auto go = [&](auto src_c) {
