@@ -1064,12 +1064,15 @@ hipError_t launch_linear_t(const XT *x, const uint8_t *packed, const GammaMap &g
             return launch_linear_m<LAYOUT, kFusedMaxM, kFdKS, kFdNSS, false, XT, YT, 2>(
                 x, packed, gamma, M, N, K, (N + 31) / 32, y, acc, s, ep);
     }
-    if (M > 1 && K % 16 == 0 &&
-        K <= (int64_t)kFsKS * kFsNSS * 4 * SkinnyCfg<LAYOUT>::kUnitCodes) {
-        const int64_t cap = (int64_t)kFusedBlocksPerCu * device_cu_count();
-        if (cap > 0 && tiles > cap)
-            return launch_linear_m<LAYOUT, kFusedMaxM, kFsKS, kFsNSS, true>(x, packed, gamma, M, N,
-                                                                          K, cap, y, acc, s, ep);
+    // (gated: more tiles than the cap of 256 compute units are taken above)
+    if constexpr (!E::kGated) {
+        if (M > 1 && K % 16 == 0 &&
+            K <= (int64_t)kFsKS * kFsNSS * 4 * SkinnyCfg<LAYOUT>::kUnitCodes) {
+            const int64_t cap = (int64_t)kFusedBlocksPerCu * device_cu_count();
+            if (cap > 0 && tiles > cap)
+                return launch_linear_m<LAYOUT, kFusedMaxM, kFsKS, kFsNSS, true>(
+                    x, packed, gamma, M, N, K, cap, y, acc, s, ep);
+        }
     }
     if (N >= kWideN) {
         // one token: two row groups per block halve the per-block work of
