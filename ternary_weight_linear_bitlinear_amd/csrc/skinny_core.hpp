@@ -598,7 +598,11 @@ hipError_t launch_skinny_t(const int8_t *xq, const float *scale, const uint8_t *
     };
     static LdsFlag lds_raised[2];  // one flag per kernel of this launcher
     if constexpr (E::kGated) {
-        if (mr) return go(skinny_gated_kernel<LAYOUT, KS, NSS, RG, MAXM, true, YT>, &lds_raised[1]);
+        if constexpr (LAYOUT == kLayoutBase3 && RG > 3) {  // rows of one round only (launch_skinny_l)
+            if (mr) return hipErrorInvalidValue;
+        } else if (mr) {
+            return go(skinny_gated_kernel<LAYOUT, KS, NSS, RG, MAXM, true, YT>, &lds_raised[1]);
+        }
         return go(skinny_gated_kernel<LAYOUT, KS, NSS, RG, MAXM, false, YT>, &lds_raised[0]);
     } else if constexpr (E::kActive) {
         if (mr)

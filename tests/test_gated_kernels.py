@@ -22,3 +22,11 @@ def test_decode_of_few_tokens_streams_no_tiles():
     assert not [a for a in found if a[4] == "1"]
     # layouts x (M = 1: three shapes and two row groups; up to 4: one, two, two wide, four) x types
     assert len(found) == 3 * 8 * 4
+
+
+def test_base3_rows_of_several_rounds_take_three_groups():
+    """Four and six row groups (the fourth argument) hold base-3 rows (1) of one round only:
+    those of several (the sixth) take three."""
+    found = kernels("skinny_gated_kernel")
+    assert not [a for a in found if a[0] == "1" and int(a[3]) > 3 and a[5] == "1"]
+    assert {a[3] for a in found if a[0] == "1" and a[5] == "1"} == {"1", "2", "3"}
