@@ -342,7 +342,6 @@ struct GatedRows {
     template <typename B>
     __device__ __forceinline__ void run(B buf, int first, int frags) const {
         if (!ep.codes && col >= F) return;  // (a group's eight threads stay together)
-#pragma unroll 2
         for (int rr = row0; rr < 32 * frags; rr += kStep) {
             const int64_t m = m0 + first + rr;
             if (m >= M) return;
