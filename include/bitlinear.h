@@ -395,7 +395,9 @@ bl_status bitlinear_gated_backward(const void *grad_y, int gy_dtype, const void 
  * bytes an element: the quantiser of bitlinear_quant_acts with a scale for each 64
  * columns of a row (the last group of a row may be shorter),
  *   s = max(max|x|, 1e-6) over the group, q = clamp(round(x / s * 127), -127, 127),
- * and a kept value stands for q * (s / 127), within s / 254 of x. */
+ * and a kept value stands for q * (s / 127). The quotient, both products and s / 127
+ * are rounded to fp32, which puts it within s / 254 + 2^-21 s of x; restored in bf16, it
+ * is rounded once more (2^-8 of itself at most). */
 
 /* Scales of a row of K columns: ceil(K / 64); 0 for K < 1. Host-only, pure. */
 int64_t bitlinear_checkpoint_groups(int64_t K);

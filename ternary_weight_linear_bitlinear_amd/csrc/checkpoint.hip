@@ -2,7 +2,8 @@
 // quantiser is that of the activations ([b158] §3.2, §5.2), over groups of 64
 // columns of a row instead of the whole row:
 //   s = max(max |x|, 1e-6),  q = clamp(round(x / s * 127), -127, 127)
-// and a kept value stands for q * s / 127, within s / 254 of x. Memory-bound: x is
+// and a kept value stands for q * s / 127, within s / 254 of x but for four fp32 roundings
+// (of x / s, its product with 127, s / 127 and its product with q: 2^-22 s). Memory-bound: x is
 // read once, 1 + 4 / 64 bytes written for each element; restoring is the reverse.
 //
 // Eight threads hold a group, eight columns each, and take its maximum across
