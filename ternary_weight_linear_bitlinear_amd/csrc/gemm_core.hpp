@@ -1562,7 +1562,10 @@ hipError_t launch_gemm_t(const int8_t *xq, const float *scale, const uint8_t *pa
             // A gated stack whose leftover columns make more than half a round: all
             // of them in 256 x 256 tiles, one launch (2048 x 2 x 11008 x 4096, 2.7 rounds: 187.8
             // -> 177.5 us; in 96- or 128-row leftover tiles of the same launch 181.4 and
-            // 183.9 us; 1500 tokens, 2.02 rounds, would go from 138 to 171 us)
+            // 183.9 us; 1500 tokens, 2.02 rounds, would go from 138 to 171 us). 1024 to 4096
+            // tokens, 1.5 to 4 rounds, all layouts, K of 1024 and 4096: 4 to 8% less time at 0.52 to
+            // 0.7 of a round left over one, 11 to 15% at 0.8 and more; 2 to 4 and 5 to 8% over three.
+            // At half a round both take the same.
             if (E::kGated && tm * (tn - tn_main) > kCUs / 2) {
                 if (gemm_dma_fits<LAYOUT, YT>(N, K, ldy))
                     return launch_gemm_dma<LAYOUT, 256>(xq, scale, packed, gamma, M, N, K, y, ldy, acc, s, ep);

@@ -614,6 +614,25 @@ hipError_t launch_skinny_t(const int8_t *xq, const float *scale, const uint8_t *
     }
 }
 
+// A gated stack's two matrices make more rows than one round of workgroups takes in
+// two or three row groups, and each further round stages the activations again. With
+// more than eight tokens four or six groups are faster (two groups -> these; 16
+// tokens, K = 4096, 2-bit / base-3 / 1-bit): 2 x 8192 rows, four, 9.0 -> 8.6 / 14.1 ->
+// 10.6 / 7.6 -> 7.7 us; 2 x 11008 rows, six, 12.5 -> 10.3 / 19.9 -> 13.2 / 11.4 -> 9.6 us; 2
+// x 14336 rows, four, 14.4 -> 11.7 / 25.5 -> 18.9 / 13.5 -> 11.2 us; 40 tokens, 2 x 11008 rows, six,
+// 24.5 -> 18.7 (2-bit) / 23.3 -> 18.4 us (1-bit). Base-3 rows of several rounds spill with more than
+// three (16 tokens, 2 x 11008 x 8192: two 29.0, three 25.0, four 36.4 us) and take two up to
+// the 16384 rows that those have in two rounds (2 x 8192 x 8192: two 20.2, three 23.7 us; x
+// 11008 27.0 and 31.4). Over 9, 16 and 40 tokens, 2 x 6500 .. 28672 rows and K of 1024 ..
+// 11008 in the three layouts (264 problems) a launch takes from 60 to 107% of two groups'
+// time, 84% on average (107%: 9 tokens in 1-bit, 0.6 us; at eight tokens 98 to 109%), and up to 17%, 2% on
+// average, more than the fastest number of groups. 0: as for a plain product.
+constexpr int gated_row_groups(int layout, int64_t M, int64_t N, bool several_rounds) {
+    if (M <= 8 || N <= 16 * 256 * 3) return 0;
+    if (layout == kLayoutBase3 && several_rounds) return N > 16 * 256 * 4 ? 3 : 0;
+    return N > 16 * 256 * 4 && N <= 16 * 256 * 6 ? 6 : 4;
+}
+
 template <int LAYOUT, typename YT, typename E>
 hipError_t launch_skinny_l(const int8_t *xq, const float *scale, const uint8_t *packed,
                            const GammaMap &gamma, int64_t M, int64_t N, int64_t K, YT *y,
@@ -625,27 +644,18 @@ hipError_t launch_skinny_l(const int8_t *xq, const float *scale, const uint8_t *
     if (M <= 4)
         return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 1, 4, YT>(xq, scale, packed, gamma, M, N, K,
                                                                y, acc, s, ep);
-    // A gated stack's two matrices make more rows than one round of workgroups takes in
-    // two or three row groups, and each further round stages the activations again. With
-    // more than eight tokens four or six groups are faster (two groups -> these; 16
-    // tokens, K = 4096, 2-bit / base-3 / 1-bit): 2 x 8192 rows, four, 9.0 -> 8.6 / 14.1 ->
-    // 10.6 / 7.6 -> 7.7 us; 2 x 11008 rows, six, 12.5 -> 10.3 / 19.9 -> 13.2 / 11.4 -> 9.6 us; 2
-    // x 14336 rows, four, 14.4 -> 11.7 / 25.5 -> 18.9 / 13.5 -> 11.2 us; 40 tokens, 2 x 11008 rows, six,
-    // 24.5 -> 18.7 (2-bit) / 23.3 -> 18.4 us (1-bit). Base-3 rows of several rounds spill with more than
-    // three (2 x 11008 x 8192: two 28.8, three 24.8, four 36.2 us). At eight tokens they were
-    // between 2% faster and 9% slower.
     if constexpr (E::kGated) {
-        const bool mr = row_bytes_of(LAYOUT, K) / SkinnyCfg<LAYOUT>::kUnitBytes > (int64_t)kSkKS * kSkNSS * 4;
-        if (M > 8 && N > 16 * 256 * 3) {
-            if (LAYOUT == kLayoutBase3 && mr)
-                return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 3, 16, YT>(xq, scale, packed, gamma, M, N, K, y,
-                                                                       acc, s, ep);
-            if (N > 16 * 256 * 4 && N <= 16 * 256 * 6)
-                return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 6, 16, YT>(xq, scale, packed, gamma, M, N, K, y,
-                                                                       acc, s, ep);
+        const int groups = gated_row_groups(
+            LAYOUT, M, N, row_bytes_of(LAYOUT, K) / SkinnyCfg<LAYOUT>::kUnitBytes > (int64_t)kSkKS * kSkNSS * 4);
+        if (groups == 3)
+            return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 3, 16, YT>(xq, scale, packed, gamma, M, N, K, y, acc,
+                                                                   s, ep);
+        if (groups == 4)
             return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 4, 16, YT>(xq, scale, packed, gamma, M, N, K, y, acc,
                                                                    s, ep);
-        }
+        if (groups == 6)
+            return launch_skinny_t<LAYOUT, kSkKS, kSkNSS, 6, 16, YT>(xq, scale, packed, gamma, M, N, K, y, acc,
+                                                                   s, ep);
     }
     // up to 16 x 256 x 3 rows: three row groups, so that one round of
     // workgroups (at most one per compute unit) covers the matrix
