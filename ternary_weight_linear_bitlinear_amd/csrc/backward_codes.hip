@@ -817,10 +817,11 @@ struct KindOf {
 
 // How a product runs: 256 x 256 tiles or 64 x 64 ones, and the workgroups that share
 // a tile's slices where there are few tiles: whichever takes the least time by a model
-// whose constants were fitted to 5982 problems of 8 to 4096 tokens and up to 4096 x 21000
-// weights, each timed with both tiles and every number of workgroups below. What it picks
-// takes 0.9% (weight gradients), 1.8% (input gradients of fp32) and 2.8% (of bf16) more on
-// average than the fastest choice for each of them.
+// whose constants were fitted to timed problems of 8 to 4096 tokens. Over 21716 others of
+// 8 to 4096 tokens and up to 4096 x 21000 weights, each timed with both tiles and every number
+// of workgroups below, what it picks takes 1.5 to 1.8% (weight gradients), 2.3% (input
+// gradients of fp32) and 3.4% (of bf16) more on average than the fastest choice, 8 to 15%
+// for one in twenty, and 1.74 times at worst (an unaligned weight gradient, 71 us for 41).
 //   Small tiles: us for 64 contraction indexes with one workgroup on a compute unit, with
 //   more, and for each where they fill the card; large ones: us for a round of one for each
 //   compute unit. What a workgroup does besides counts as so many slices more. Rows that
