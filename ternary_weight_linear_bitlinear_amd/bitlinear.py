@@ -540,6 +540,13 @@ def _rows_of(seg_rows):
 _row_bytes = functools.lru_cache(maxsize=1024)(bitlinear_packed_row_bytes)
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(call: str, *sizes) -> int:
+    """A size helper of the library for plain numbers (a tensor would be a key by its
+    identity, whatever it holds): the public helpers make numbers of what they are given."""
+    return int(getattr(_lib, call)(*sizes))
+
+
 def _product_epilogue(where, call, lead, M, K, dev, packed, gammas, seg_rows, layout, bias, act, residual,
                       residual_scale, out_dtype, y, z):
     lay = _one_of(where, "layout", layout, LAYOUTS)
@@ -654,9 +661,8 @@ class EpilogueGrads(NamedTuple):
     grad_residual: torch.Tensor | None
 
 
-@functools.lru_cache(maxsize=1024)
 def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
-    return int(_lib.bitlinear_epilogue_backward_workspace_bytes(M, N))
+    return _workspace_bytes("bitlinear_epilogue_backward_workspace_bytes", operator.index(M), operator.index(N))
 
 
 def bitlinear_epilogue_backward(grad_y: torch.Tensor, z: torch.Tensor | None, act="none",
@@ -830,9 +836,8 @@ def _param_grad(where, name, t, p, row, dev):
     return t, t.data_ptr()
 
 
-@functools.lru_cache(maxsize=1024)
 def bitlinear_block_norm_backward_workspace_bytes(M: int, K: int) -> int:
-    return int(_lib.bitlinear_block_norm_backward_workspace_bytes(M, K))
+    return _workspace_bytes("bitlinear_block_norm_backward_workspace_bytes", operator.index(M), operator.index(K))
 
 
 def bitlinear_block_norm_backward(grad_h_out: torch.Tensor | None, grad_n: torch.Tensor | None,
@@ -1047,9 +1052,8 @@ def linear_gated(x: torch.Tensor, packed: torch.Tensor, gammas: torch.Tensor, F:
     return bitlinear_forward_gated(xq, scale, packed, gammas, F, K, layout, bias, act, out_dtype, y, z, kept)
 
 
-@functools.lru_cache(maxsize=1024)
 def bitlinear_gated_backward_workspace_bytes(M: int, F: int) -> int:
-    return int(_lib.bitlinear_gated_backward_workspace_bytes(M, F))
+    return _workspace_bytes("bitlinear_gated_backward_workspace_bytes", operator.index(M), operator.index(F))
 
 
 def bitlinear_gated_backward(grad_y: torch.Tensor, z: torch.Tensor | Checkpoint, act="silu",
@@ -1123,14 +1127,14 @@ def bitlinear_checkpoint_restore(kept: Checkpoint, out_dtype=None, y: torch.Tens
     return y
 
 
-@functools.lru_cache(maxsize=1024)
 def bitlinear_backward_weight_codes_workspace_bytes(M: int, N: int, K: int, out_dtype=torch.float32) -> int:
-    return int(_lib.bitlinear_backward_weight_codes_workspace_bytes(M, N, K, _code(out_dtype)))
+    return _workspace_bytes("bitlinear_backward_weight_codes_workspace_bytes", operator.index(M), operator.index(N),
+                            operator.index(K), _code(out_dtype))
 
 
-@functools.lru_cache(maxsize=1024)
 def bitlinear_backward_input_segmented_workspace_bytes(M: int, N: int, K: int, grad_dtype=torch.float32) -> int:
-    return int(_lib.bitlinear_backward_input_segmented_workspace_bytes(M, N, K, _code(grad_dtype)))
+    return _workspace_bytes("bitlinear_backward_input_segmented_workspace_bytes", operator.index(M),
+                            operator.index(N), operator.index(K), _code(grad_dtype))
 
 
 def bitlinear_backward_weight_codes(grad_y: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,
