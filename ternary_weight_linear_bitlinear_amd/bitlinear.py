@@ -1128,13 +1128,16 @@ def bitlinear_checkpoint_restore(kept: Checkpoint, out_dtype=None, y: torch.Tens
 
 
 def bitlinear_backward_weight_codes_workspace_bytes(M: int, N: int, K: int, out_dtype=torch.float32) -> int:
-    return _workspace_bytes("bitlinear_backward_weight_codes_workspace_bytes", operator.index(M), operator.index(N),
-                            operator.index(K), _code(out_dtype))
+    where = "bitlinear_backward_weight_codes_workspace_bytes"
+    return _workspace_bytes(where, operator.index(M), operator.index(N), operator.index(K),
+                            _code(_out_dtype(where, out_dtype, None)))
 
 
 def bitlinear_backward_input_segmented_workspace_bytes(M: int, N: int, K: int, grad_dtype=torch.float32) -> int:
-    return _workspace_bytes("bitlinear_backward_input_segmented_workspace_bytes", operator.index(M),
-                            operator.index(N), operator.index(K), _code(grad_dtype))
+    where = "bitlinear_backward_input_segmented_workspace_bytes"
+    if grad_dtype not in _DTYPES:
+        _refuse(where, f"grad_dtype is {grad_dtype}")
+    return _workspace_bytes(where, operator.index(M), operator.index(N), operator.index(K), _code(grad_dtype))
 
 
 def bitlinear_backward_weight_codes(grad_y: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,

@@ -27,3 +27,13 @@ def test_no_count(helper, rest):
     for bad in (2.0, "200", None, torch.tensor(200.0)):
         with pytest.raises(TypeError):
             helper(bad, *rest)
+
+
+@pytest.mark.parametrize("helper", [bl.bitlinear_backward_weight_codes_workspace_bytes,
+                                    bl.bitlinear_backward_input_segmented_workspace_bytes])
+def test_a_type_that_the_call_refuses(helper):
+    """No size for a type that the call itself would not take."""
+    for bad in (torch.float16, torch.float64, torch.int8, "f32"):
+        with pytest.raises(bl.BitLinearError):
+            helper(300, 4096, 4096, bad)
+    assert helper(300, 4096, 4096, torch.float32) == helper(300, 4096, 4096)
