@@ -43,7 +43,10 @@
 // What bounds it: large tiles keep the matrix cores busy for 57-60% of a compute unit's
 // cycles at the clock that their power leaves (weight gradient 4096^3: 2 x 137 GFLOP in 239 us,
 // 1.15 PFLOP/s; input gradient of 2048 tokens over 2 x 11008 rows of 4096: 369 GFLOP in 297
-// us, 1.24 PFLOP/s; a library product of 8192^3 in bf16 reaches 1.2). Small tiles wait: of a
+// us, 1.24 PFLOP/s; a library product of 8192^3 in bf16 reaches 1.2). Unaligned rows cost the
+// weight gradient 6 to 19%, the input gradient from fp32 20% and from bf16 19 (1-bit) to 54%
+// (2-bit, base-3): ends that load element by element, branches behind the loads, and 4 to 11
+// spilled registers in its large tiles. Small tiles wait: of a
 // stage's 0.8 us (fp32, three pieces, aligned) 0.2 are loads and their addresses, 0.2 the
 // conversion, and the matrix cores' third hides behind the rest. Tried there and not
 // kept: loads two stages ahead (the same times), a stage's fragments read at once (29.5 -> 31.8 us),
