@@ -160,3 +160,43 @@ def test_bf16_gradients_are_one_piece(bl):
     v = p.rand(4100, 9)
     v[:, 1:] *= 2.0 ** -60
     check_input(bl, p, grad_y.scatter_(1, at, v).to(BF16), 9)
+
+
+def test_a_graph_follows_the_values(bl):
+    """Which pieces a tile takes is found from the values at every replay: a graph captured
+    with values of one range gives, for others, what the eager calls give."""
+    M, K, segs = 1024, 2048, [2048, 2048]
+    p = Packed(bl, 0, segs, K, seed=4)
+    xq, scale = bl.bitlinear_quant_acts(p.rand(M, K))
+    gy = p.rand(M, sum(segs))
+    spread = torch.logspace(-14, 0, sum(segs), device="cuda")[None] * torch.logspace(-14, 0, M, device="cuda")[:, None]
+    ws = torch.empty(max(bl.bitlinear_backward_weight_codes_workspace_bytes(M, sum(segs), K),
+                         bl.bitlinear_backward_input_segmented_workspace_bytes(M, sum(segs), K)),
+                     dtype=torch.uint8, device="cuda")
+    gw, gx = torch.empty(sum(segs), K, device="cuda"), torch.empty(M, K, device="cuda")
+
+    def run():
+        bl.bitlinear_backward_weight_codes(gy, xq, scale, grad_w=gw, workspace=ws)
+        bl.bitlinear_backward_input_segmented(gy, p.packed, p.gammas, segs, K, grad_x=gx, workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for rep in range(6):
+        g = p.rand(M, sum(segs))
+        if rep % 3 == 1:
+            g = g * spread
+        elif rep % 3 == 2:  # half of the rows' tiles, half of the columns'
+            g[:M // 2, :segs[0]] = (g * spread)[:M // 2, :segs[0]]
+        gy.copy_(g)
+        run()
+        want = gw.clone(), gx.clone()
+        gw.zero_()
+        gx.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(gw, want[0]) and torch.equal(gx, want[1]), rep
+    v = gy.cpu().double() * p.row_gamma
+    ref.close(gx, v @ p.codes.double(), (4 * sum(segs) + 12) * U * (v.abs() @ p.codes.double().abs()), "grad_x")
