@@ -683,7 +683,10 @@ __device__ __forceinline__ bool codes_gemm_tile(const CodesArgs a) {
     return true;
 }
 
-// HALF: NP fp16 pieces, or EXACT bf16 ones in tiles whose rows' values lie too far apart.
+// HALF: NP fp16 pieces, or EXACT bf16 ones in tiles whose rows' values lie too far apart
+// (the tile gives up before its first load). One kernel for both, as a second one whose tiles
+// end at once would be a launch more for every call; the input gradient takes as long as with
+// fp16 alone, the weight gradient 1 to 2 us more (300 x 4096 x 4096 36.0 -> 37.2 us).
 template <typename T, bool A_T, int BSRC, int NP, bool HALF, int EXACT, bool VEC, typename GT, typename OT>
 __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs a) {
     if (!codes_gemm_tile<T, A_T, BSRC, NP, HALF, VEC, GT, OT>(a))
@@ -691,8 +694,7 @@ __global__ __launch_bounds__(T::kThreads) void codes_gemm_kernel(const CodesArgs
 }
 
 // The largest |v| of each column of grad_y [M, N] over a run of tokens and the least that
-// is not zero: eight columns
-// and every eighth token of the run for each thread.
+// is not zero: eight columns and every eighth token of the run for each thread.
 template <typename GT, bool VEC>
 __global__ __launch_bounds__(256) void codes_peak_cols_kernel(const GT *grad_y, const float *scale, int64_t M,
                                                               int64_t N, uint2 *peak) {
